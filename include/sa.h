@@ -69,8 +69,9 @@ typedef enum {
     SA_ERR_UNSUPPORTED = 2,   /* valid, but outside what the built kernels handle */
     SA_ERR_CUDA = 3,          /* a CUDA runtime/driver call or a launch failed */
     SA_ERR_TIMEOUT = 4,       /* a device-side wait ran out of its time limit */
-    SA_ERR_BAD_LIST = 5,      /* a kept list held an index outside [0, nt) */
-    SA_ERR_WORKSPACE = 6      /* workspace NULL or smaller than the _workspace_size query */
+    SA_ERR_BAD_LIST = 5,      /* a kept list or a page table held an index out of range */
+    SA_ERR_WORKSPACE = 6,     /* workspace NULL or smaller than the _workspace_size query */
+    SA_ERR_NONFINITE = 7      /* infinities or NaN where only finite numbers can be stored */
 } sa_status;
 
 typedef enum { SA_F32 = 0, SA_BF16 = 1 } sa_dtype;
@@ -342,6 +343,91 @@ size_t sa_sga_workspace_size(const sa_shape* shape, int32_t grid_h, int32_t grid
 sa_status sa_sga_fwd(const sa_shape* shape, int32_t grid_h, int32_t grid_w, int32_t s_h, int32_t s_w,
                      const void* q, const void* k, const void* v, void* workspace, size_t workspace_bytes,
                      void* o, float* lse_or_null, sa_stream_t stream);
+
+/*
+ * The frame cache.  No passage of the pages corresponds to it; it is for calls that do not have
+ * every frame at hand at once: frames arrive one by one (or in groups), K and V of a layer's
+ * earlier frames stay in device memory, and the new rows attend to them.  At 1,024 frames of
+ * 1,374 tokens and 16 heads K and V in bf16 are 5.8 GB a layer; in 4 bits they are 1.6 GB.
+ *
+ * Scenes.  The cache serves `scenes` independent scenes of any lengths; lens[s] (DEVICE int32
+ *   [scenes]) is the number of tokens that scene s has in the cache.  Lengths and page table are
+ *   read on the device when the kernels run, and every layer of a model can share them.
+ * Pages.  The pool is n_pages pages of `page` tokens for all `heads` key heads, one contiguous
+ *   array of sa_kv_pool_size bytes; page_table (DEVICE int32 [scenes][max_pages]) names the page
+ *   of every `page` tokens of a scene, in any order.  Entries past a scene's length are not read.
+ *   An entry outside [0, n_pages) is reported as SA_ERR_BAD_LIST by sa_check_device_error and its
+ *   tokens are neither written nor read (attention leaves them out).  A length outside
+ *   [0, max_pages * page] is clamped and reported as SA_ERR_INVALID_ARG.  Scenes may share pages
+ *   that neither of them writes.
+ * Numbers.  A stored number is code * s with one scale s per 16 channels of one token,
+ *   s = (8 + b % 8) / 8 * 2^(b / 8 - 16) for a byte b:
+ *     bits = 4: s the smallest scale with 7.5 s >= max|x|, code = clamp(round(x / s), -7, 7)
+ *     bits = 8: s the smallest power of two with 127.5 s >= max|x|, code = clamp(round(x / s), -127, 127)
+ *   (so b is a multiple of 8 with 8 bits; round half to even, x / s exact; the largest scale where none is large enough).  Each is
+ *   exactly a bf16 number.  72 (136) bytes per token and head for K and V together.
+ *   Infinities are stored as the largest magnitude, NaN as 0, both reported as SA_ERR_NONFINITE
+ *   by sa_check_device_error.  The layout of the bytes of a page is given in k_kv_cache.cuh.
+ */
+typedef struct {
+    int32_t scenes;     /* >= 1 */
+    int32_t heads;      /* key/value heads (>= 1); scenes * heads < 2^31 */
+    int32_t head_dim;   /* 64 is built (else SA_ERR_UNSUPPORTED) */
+    int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
+    int32_t n_pages;    /* pages of the pool (>= 1) */
+    int32_t max_pages;  /* columns of the page table (>= 1); max_pages * page <= 2^31 - 256 */
+    int32_t bits;       /* 4 or 8 */
+} sa_kv_cache;
+
+/* Bytes of the pool: n_pages * heads * page * 2 * (64 * bits / 8 + 4); 0 for an invalid cache. */
+size_t sa_kv_pool_size(const sa_kv_cache* cache);
+
+/*
+ * Write the last rows of every scene into its pages.  k, v: [scenes * heads][n][64] of `dtype`
+ * (f32 or bf16).  lens already counts the new rows: row r of scene s, r < m (m = n, or
+ * n_len[s] <= n where n_len, DEVICE int32 [scenes], is given), is token lens[s] - m + r.  Rows
+ * r >= m are not read.  Other tokens of a page keep their bytes.  m > lens[s] and n_len[s]
+ * outside [0, n] are reported as SA_ERR_INVALID_ARG by sa_check_device_error (rows before token 0
+ * are dropped, n_len is clamped).
+ */
+sa_status sa_kv_append(const sa_kv_cache* cache, sa_dtype dtype, const void* k, const void* v, int32_t n,
+                       const int32_t* n_len_or_null, const int32_t* lens, const int32_t* page_table,
+                       void* pool, sa_stream_t stream);
+
+/*
+ * Read rows back: row r < m of scene s (m as for sa_kv_append) is token start[s] + r, or
+ * lens[s] - m + r without `start` (DEVICE int32 [scenes]).  k, v: [scenes * heads][n][64] of
+ * `dtype`, either of them NULL to leave it out.  Exact in both types.  Rows r >= m, rows whose
+ * token is outside [0, lens[s]) and rows on a bad page are left as they were.
+ */
+sa_status sa_kv_read(const sa_kv_cache* cache, sa_dtype dtype, int32_t n, const int32_t* n_len_or_null,
+                     const int32_t* start_or_null, const int32_t* lens, const int32_t* page_table,
+                     const void* pool, void* k_or_null, void* v_or_null, sa_stream_t stream);
+
+/* Bytes of workspace sa_kv_attn_fwd needs for these heads and rows (parts of problems that several
+ * thread blocks share); it does not depend on the lengths.  0 for invalid arguments. */
+size_t sa_kv_attn_workspace_size(const sa_kv_cache* cache, int32_t q_heads, int32_t rows);
+
+/*
+ * Attention over the cache.  q, o: [scenes * q_heads][rows][64] bf16, lse f32 [scenes * q_heads][rows]
+ * (optional).  Query head j of a scene uses key head j / (q_heads / heads); q_heads is a multiple of
+ * heads.  Row r of scene s, r < m (m = rows, or q_len[s] <= rows where q_len, DEVICE int32 [scenes],
+ * is given), stands at position p = lens[s] - m + r, as if the rows were the scene's last m tokens,
+ * and sees
+ *   frame == 0: every cached token j < lens[s];
+ *   frame > 0:  the tokens of its own and of earlier frames of `frame` tokens,
+ *               j < min(lens[s], (p / frame + 1) * frame); none if p < 0.  (1: causal by token.)
+ *   O = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
+ * with softmax_scale as sa_shape has it (0 selects 1/8).  A row that sees no token gets O = 0,
+ * lse = -inf.  Rows r >= m of o and lse are left as they were.  bf16 products of the stored numbers
+ * with f32 accumulation, f32 softmax, probabilities rounded to bf16 before they meet V.  Results do
+ * not depend on the order in which thread blocks run.  workspace: >= sa_kv_attn_workspace_size bytes.
+ */
+sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_heads, int32_t rows,
+                         const int32_t* q_len_or_null, int32_t frame, float softmax_scale,
+                         const int32_t* lens, const int32_t* page_table, const void* pool,
+                         void* workspace, size_t workspace_bytes, void* o, float* lse_or_null,
+                         sa_stream_t stream);
 
 /* Test facility for the failure path (not for production use): while enable != 0, later
  * launches of the tensor-core attention kernels (bf16, tile 128: the forward and the dQ kernel

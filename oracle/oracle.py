@@ -545,3 +545,84 @@ def selection_matches(g: Geometry, s_row: np.ndarray, i: int, k: int, got: np.nd
             if sb - sa > rel * max(abs(sa), abs(sb)) + floor * smax:
                 return False, "swap %d<->%d beyond tolerance (%.9g vs %.9g)" % (a, b, sa, sb)
     return True, "%d near-tie swaps" % len(extra)
+
+
+# ----------------------------------------------------------------------------- the frame cache
+
+def cache_scale(byte) -> np.ndarray:
+    """The scale that a byte stands for: (8 + b % 8) / 8 * 2^(b // 8 - 16)."""
+    b = np.asarray(byte).astype(np.int64)
+    return np.ldexp(1.0 + (b % 8) / 8.0, (b // 8 - 16).astype(np.int32))
+
+
+def cache_numbers(x: np.ndarray, bits: int) -> np.ndarray:
+    """What the cache holds for finite rows x [..., 64]: code * s per block of 16 channels, s the smallest scale
+    (8 bits: the smallest power of two among them) whose top code + 1/2 reaches max|x|."""
+    y = np.asarray(x, np.float64).reshape(x.shape[:-1] + (x.shape[-1] // 16, 16))
+    top = 7 if bits == 4 else 127
+    scales = cache_scale(np.arange(256))
+    if bits == 8:
+        scales = scales[::8]
+    most = np.abs(y).max(-1)
+    i = np.minimum(np.searchsorted((top + 0.5) * scales, most, side="left"), len(scales) - 1)
+    s = scales[i][..., None]
+    return (np.clip(np.rint(y / s), -top, top) * s).reshape(x.shape)
+
+
+def cache_unpack(pages: np.ndarray, page: int, bits: int):
+    """K and V [..., page, 64] of the bytes of pages [..., page * 2 * (8 * bits + 4)] (uint8)."""
+    db = 8 * bits
+    lead = pages.shape[:-1]
+    out = []
+    for part in range(2):
+        lo = part * page * (db + 4)
+        code_b = pages[..., lo:lo + page * db].reshape(lead + (page // 2, 2 * db))
+        byte = pages[..., lo + page * db:lo + page * (db + 4)]
+        unit = code_b[..., 0::2].astype(np.int64) | code_b[..., 1::2].astype(np.int64) << 8
+        if bits == 4:
+            code = np.stack([(unit >> (4 * j) & 15) - 8 for j in range(4)], -1)
+        else:
+            a = np.where(unit >> 15 & 1, -(unit & 127), unit & 127)
+            b = np.where(unit >> 7 & 1, -(unit >> 8 & 127), unit >> 8 & 127)
+            code = np.stack([a, b], -1)
+        per = code.shape[-1]
+        if part == 0:  # K: [token][...], units in pairs of even and odd channels
+            code = code.reshape(lead + (page, 64 // (2 * per), 2, per))
+            code = np.swapaxes(code, -1, -2).reshape(lead + (page, 64))
+            scale = cache_scale(byte).reshape(lead + (page, 4))
+        else:          # V: [token pair][...], units in pairs of even and odd tokens
+            code = code.reshape(lead + (page // 2, 64 // per, 2, per))
+            code = np.moveaxis(code, -2, -3).reshape(lead + (page, 64))
+            scale = cache_scale(byte).reshape(lead + (page // 2, 4, 2))
+            scale = np.swapaxes(scale, -1, -2).reshape(lead + (page, 4))
+        out.append(code * np.repeat(scale, 16, -1))
+    return out[0], out[1]
+
+
+def cache_attend(q: np.ndarray, K: np.ndarray, V: np.ndarray, scale: float, frame: int = 0):
+    """Attention of query rows q [heads][rows][64], the last rows of a scene, over its K, V [key heads][tokens][64].
+    Returns (O, LSE, A, B): A = sum_j w_j |v_j| and B = scale * max_j sum_e |q_e k_je| of each row, which the
+    error bounds are made of."""
+    H, R, d = q.shape
+    L = K.shape[1]
+    group = H // K.shape[0]
+    pos = L - R + np.arange(R)
+    seen = np.full(R, L) if frame == 0 else np.where(pos < 0, 0, np.minimum(L, (pos // frame + 1) * frame))
+    O, A = np.zeros((H, R, d)), np.zeros((H, R, d))
+    lse, B = np.full((H, R), -np.inf), np.zeros((H, R))
+    mask = np.arange(L) < seen[:, None]
+    for h in range(H):
+        k, v = K[h // group], V[h // group]
+        if L == 0:
+            continue
+        s = np.where(mask, scale * (q[h] @ k.T), -np.inf)
+        m = s.max(-1, keepdims=True)
+        m = np.where(np.isfinite(m), m, 0.0)
+        p = np.exp(s - m)
+        l = p.sum(-1)
+        live = l > 0
+        w = p / np.where(live, l, 1.0)[:, None]
+        O[h], A[h] = w @ v, w @ np.abs(v)
+        lse[h, live] = m[live, 0] + np.log(l[live])
+        B[h] = scale * (np.abs(q[h]) @ np.abs(k).T).max(-1)
+    return O, lse, A, B

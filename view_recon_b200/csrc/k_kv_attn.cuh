@@ -1,0 +1,618 @@
+// Attention of query rows over the frame cache (k_kv_cache.cuh): O = softmax(scale q K^T) V over the
+// cached tokens of each scene, every key or those of a row's own and earlier frames.
+//
+// Work is a list of (scene, tile of query rows, head) problems, each a run of 128-key tiles; their
+// number is known on the device only (lengths are device memory, so that a captured call follows
+// them).  The concatenated list of key tiles is cut into equal runs, one per CTA, whatever the
+// lengths; a CTA that holds all tiles of a problem writes its rows, otherwise it leaves (O, max,
+// sum) of its part in the workspace and kv_merge_kernel joins the parts in a fixed order (no
+// atomics: results do not depend on timing).
+#pragma once
+#include "k_attn_tc.cuh"
+#include "k_kv_cache.cuh"
+
+namespace kv {
+
+struct AttnArgs {
+    const uint8_t* pool;
+    const int32_t* table;  // [scenes][max_pages]
+    const int32_t* lens;   // [scenes]
+    const int32_t* q_len;  // [scenes] or null
+    const __nv_bfloat16* q;
+    __nv_bfloat16* o;
+    float* lse;            // or null
+    float* part_o;         // [2 * ctas][tile_rows][64]
+    float* part_ml;        // [2 * ctas][2][tile_rows]: running max (base 2), sum
+    int32_t scenes, kv_heads, group, rows;
+    int32_t tile_rows, row_tiles;  // query rows per problem, problems per (scene, head)
+    int32_t page_log2, n_pages, max_pages, frame;
+    int32_t ctas, min_tiles;  // grid of the attention kernel, least tiles of a CTA
+    int64_t page_bytes;
+    float scale_log2;
+};
+
+// One scene's share: cached tokens and query rows.
+struct Scene {
+    int32_t len, n;
+};
+__device__ __forceinline__ Scene scene_of(const AttnArgs& a, int s) {
+    return Scene{scene_len(a.lens, s, a.max_pages, a.page_log2), scene_rows(a.q_len, s, a.rows)};
+}
+// Keys that query row r of a scene sees: positions below this.  Row r is position len - n + r.
+__device__ __forceinline__ int32_t key_limit(const AttnArgs& a, const Scene& sc, int32_t r) {
+    if (a.frame == 0) return sc.len;
+    const int32_t pos = sc.len - sc.n + r;
+    if (pos < 0) return 0;
+    return (int32_t)min(((int64_t)(pos / a.frame) + 1) * a.frame, (int64_t)sc.len);
+}
+// A problem's rows are numbered row-major, the query heads of one key head innermost: row x of the
+// (scene, key head) is query row x / group of query head x % group.  Limits ascend with x.
+__device__ __forceinline__ int32_t valid_rows(const AttnArgs& a, const Scene& sc, int32_t rt) {
+    return max(0, (int32_t)min((int64_t)a.tile_rows, (int64_t)sc.n * a.group - (int64_t)rt * a.tile_rows));
+}
+__device__ __forceinline__ int32_t key_tiles(const AttnArgs& a, const Scene& sc, int32_t rt) {
+    const int32_t nv = valid_rows(a, sc, rt);
+    if (nv == 0) return 0;
+    return (int32_t)(((int64_t)key_limit(a, sc, (int32_t)(((int64_t)rt * a.tile_rows + nv - 1) / a.group)) + 127) / 128);
+}
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int s, int h, int64_t x) {
+    const int64_t head = ((int64_t)s * a.kv_heads + h) * a.group + x % a.group;
+    return head * a.rows + x / a.group;
+}
+
+// Named barrier over `nthreads` threads that tells each of them whether all came with true.
+__device__ __forceinline__ bool all_agree(uint32_t id, uint32_t nthreads, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)mine)
+        : "memory");
+    return r != 0;
+}
+// Waits until the kernel before this one in the stream, whose end this one was launched ahead of, is
+// done and its writes are seen.  Every thread of such a kernel comes through here before it ends, so
+// that what follows in the stream follows both.
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The list of problems, entry e = (scene e / row_tiles, row tile e % row_tiles), heads within.
+struct Cut {
+    int64_t total;  // key tiles of all problems
+    int64_t per;    // of one CTA
+};
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+__device__ __forceinline__ int64_t entry_tiles(const AttnArgs& a, int64_t e) {
+    const int s = (int)(e / a.row_tiles), rt = (int)(e % a.row_tiles);
+    return (int64_t)key_tiles(a, scene_of(a, s), rt) * a.kv_heads;
+}
+// Every warp of the block calls it; `red` is shared memory of one int64 per warp.
+__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int64_t* red) {
+    const int64_t n = (int64_t)a.scenes * a.row_tiles;
+    int64_t sum = 0;
+    for (int64_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_tiles(a, e);
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += red[w];
+    return Cut{sum, max((sum + a.ctas - 1) / a.ctas, (int64_t)a.min_tiles)};
+}
+// The entry that holds key tile x of the list (x < total), and the tile's index within it.  One warp.
+__device__ __forceinline__ int64_t find_entry(const AttnArgs& a, int64_t x, int64_t* within) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = (int64_t)a.scenes * a.row_tiles;
+    int64_t before = 0;
+    for (int64_t e0 = 0; e0 < n; e0 += 32) {
+        int64_t c = e0 + lane < n ? entry_tiles(a, e0 + lane) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
+            if (lane >= d) c += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + c > x);
+        if (past) {
+            const int first = __ffs(past) - 1;
+            const int64_t prev = __shfl_sync(0xffffffffu, c, max(first - 1, 0));
+            *within = x - before - (first > 0 ? prev : 0);
+            return e0 + first;
+        }
+        before += __shfl_sync(0xffffffffu, c, 31);
+    }
+    *within = 0;
+    return n;
+}
+
+// One problem's share of a CTA's run of key tiles.
+struct Segment {
+    int32_t s, rt, h;
+    int32_t t0, t1, tiles;  // key tiles [t0, t1) of the problem's `tiles`
+    Scene sc;
+};
+// Walks the CTA's run; every role of the CTA makes the same walk.
+struct Walk {
+    int64_t left;  // key tiles still to come
+    int64_t e;
+    int32_t h, t;
+    __device__ __forceinline__ bool next(const AttnArgs& a, Segment* g) {
+        if (left <= 0) return false;
+        const int64_t n = (int64_t)a.scenes * a.row_tiles;
+        for (;;) {
+            if (e >= n) return false;
+            g->s = (int32_t)(e / a.row_tiles);
+            g->rt = (int32_t)(e % a.row_tiles);
+            g->sc = scene_of(a, g->s);
+            g->tiles = key_tiles(a, g->sc, g->rt);
+            if (g->tiles > 0 && h < a.kv_heads) break;
+            ++e;
+            h = t = 0;
+        }
+        g->h = h;
+        g->t0 = t;
+        g->t1 = (int32_t)min((int64_t)g->tiles, t + left);
+        left -= g->t1 - g->t0;
+        t = 0;
+        ++h;
+        return true;
+    }
+};
+// Workspace slot of a segment that is part of a problem: a CTA leaves at most two, the first and the
+// last of its run.
+__device__ __forceinline__ int part_slot(bool first) { return 2 * (int)blockIdx.x + (first ? 0 : 1); }
+
+// ------------------------------------------------------------------------------ few rows
+//
+// Up to 32 query rows a problem: bound by the reading and decoding of the pages, so the rows ride on
+// the narrow side of mma.sync (m16n8k16, keys on m, rows on n): S^T = K Q^T with 16 keys x 8 rows,
+// O^T += V^T P^T with 16 channels x 8 rows.  A lane's decoded words are its operand registers as they
+// stand (the page layout is made for it): no shuffle and no shared-memory round trip between a
+// page's bytes and the tensor cores; P^T is transposed by one movmatrix per 8 x 8.
+// Four warps take 32 keys each of every 128-key tile; a fifth keeps a ring of tiles in flight with
+// bulk copies of whole pages (K, V and scales of a page and head are one run of bytes).
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int BITS, int NT>  // NT: groups of 8 query rows
+struct FewLayout {
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStageBytes = 128 * Fmt<BITS>::kTokenBytes;
+    static constexpr int kStages = BITS == 4 ? 4 : 3;
+    static constexpr int kRing = 0;
+    static constexpr int kMergeO = kRing + kStages * kStageBytes;       // [warp][row][64 + 4] f32
+    static constexpr int kMergeRow = 68;
+    static constexpr int kMergeMl = kMergeO + kWarps * kRows * kMergeRow * 4;  // [warp][2][row]
+    static constexpr int kBars = kMergeMl + kWarps * 2 * kRows * 4;     // full[], empty[]
+    static constexpr int kMeta = kBars + 16 * kStages;                  // per stage: bad sub-pages
+    static constexpr int kMisc = kMeta + 4 * kStages + (kStages & 1 ? 4 : 0);  // abort flag, walk, reduction
+    static constexpr int kEnd = kMisc + 96;
+    static constexpr int smem_bytes() { return kEnd; }
+    static_assert(kStageBytes % 16 == 0 && kMergeO % 16 == 0 && kBars % 8 == 0 && kMisc % 8 == 0, "alignment");
+};
+
+template <int BITS, int NT>
+__global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_rows_kernel(const AttnArgs a) {
+    using L = FewLayout<BITS, NT>;
+    using F = Fmt<BITS>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* empty = full + L::kStages;
+    volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + L::kMeta);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
+    int64_t* walk_smem = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);   // entry, tile within it
+    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 24);        // one per warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], L::kWarps);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    const Cut cut = cut_of(a, red);
+    const int64_t x0 = blockIdx.x * cut.per;
+    Walk walk;
+    walk.left = min(cut.per, cut.total - x0);
+    if (warp == 0 && walk.left > 0) {
+        int64_t within;
+        const int64_t e = find_entry(a, x0, &within);
+        if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
+    }
+    __syncthreads();
+    if (walk.left > 0) {
+        walk.e = walk_smem[0];
+        const int64_t within = walk_smem[1];
+        const int32_t tiles = (int32_t)(entry_tiles(a, walk.e) / a.kv_heads);
+        walk.h = (int32_t)(within / tiles);
+        walk.t = (int32_t)(within % tiles);
+    }
+
+    const int page = 1 << a.page_log2, sub_pages = 128 >> a.page_log2;
+    Segment g;
+    int it = 0;  // tiles so far: ring stage it % kStages
+    if (warp == L::kWarps) {
+        // ---------------------------------------------------------------- loads
+        bool ok = true;
+        while (ok && walk.next(a, &g)) {
+            const int32_t* row = a.table + (int64_t)g.s * a.max_pages;
+            const int32_t lim = (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len);
+            for (int t = g.t0; t < g.t1; ++t, ++it) {
+                const int st = it % L::kStages;
+                const int key = t * 128 + lane * page;
+                const bool mine = lane < sub_pages && key < lim;
+                const int32_t pid = mine ? __ldg(row + (key >> a.page_log2)) : 0;
+                const bool good = mine && pid >= 0 && pid < a.n_pages;
+                const uint32_t bad = __ballot_sync(0xffffffffu, mine && !good);
+                const int n = __popc(__ballot_sync(0xffffffffu, good));
+                if (!mbar_wait_warp(&empty[st], ((it / L::kStages) & 1) ^ 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (bad) sa_flag_error(SA_ERR_BAD_LIST);
+                    meta[st] = bad;
+                    mbar_arrive_expect_tx(&full[st], (uint32_t)(n * a.page_bytes));
+                }
+                __syncwarp();
+                if (good)
+                    bulk_load(smem + L::kRing + st * L::kStageBytes + lane * a.page_bytes,
+                              a.pool + ((int64_t)pid * a.kv_heads + g.h) * a.page_bytes, (uint32_t)a.page_bytes,
+                              &full[st]);
+            }
+        }
+        // every copy has landed before the CTA exits
+        for (int i = max(0, it - L::kStages); i < it; ++i) tc::drain_wait(&full[i % L::kStages], (i / L::kStages) & 1);
+    } else {
+        // ---------------------------------------------------------------- products
+        const int qg = lane >> 2, qc = lane & 3;
+        bool ok = true, first_seg = true;
+        while (ok && walk.next(a, &g)) {
+            const int32_t nv = valid_rows(a, g.sc, g.rt);
+            const int64_t r0 = (int64_t)g.rt * a.tile_rows;
+            // Q^T operand: row 8 i + qg, channels 16 qc .. 16 qc + 15
+            uint32_t qb[NT][8];
+            int32_t lim[NT][2];  // key limits of this lane's columns, rows 8 i + 2 qc and the next
+            int32_t least = 0x7FFFFFFF;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (8 * i + qg < nv) {
+                    const uint4* src =
+                        reinterpret_cast<const uint4*>(a.q + out_row(a, g.s, g.h, r0 + 8 * i + qg) * 64 + 16 * qc);
+                    u[0] = __ldg(src);
+                    u[1] = __ldg(src + 1);
+                }
+                const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) qb[i][j] = w[j];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int32_t x = 8 * i + 2 * qc + j;
+                    lim[i][j] = x < nv ? key_limit(a, g.sc, (int32_t)((r0 + x) / a.group)) : 0x7FFFFFFF;
+                    least = min(least, lim[i][j]);
+                }
+            }
+            least = min(least, g.sc.len);
+            least = __reduce_min_sync(0xffffffffu, least);
+            float o[NT][4][4], m[NT][2], l[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
+                m[i][0] = m[i][1] = -INFINITY;
+                l[i][0] = l[i][1] = 0.0f;
+            }
+            for (int t = g.t0; t < g.t1; ++t, ++it) {
+                const int st = it % L::kStages;
+                if (!mbar_wait_warp(&full[st], (it / L::kStages) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t* ring = smem + L::kRing + st * L::kStageBytes;
+                const int key0 = t * 128 + 32 * warp;  // this warp's keys of the tile
+                if (key0 < g.sc.len) {
+                    float sc[NT][2][4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int kk = 32 * warp + 16 * u, slot = kk & (page - 1);
+                        const uint8_t* base = ring + (kk >> a.page_log2) * a.page_bytes;
+                        uint32_t ka[2][8];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int tok = slot + 8 * e + qg;
+                            uint32_t w[F::kWords];
+                            const uint2* src = reinterpret_cast<const uint2*>(base + tok * F::kDB + qc * (F::kDB / 4));
+#pragma unroll
+                            for (int i = 0; i < F::kWords; i += 2) {
+                                const uint2 v = src[i / 2];
+                                w[i] = v.x;
+                                w[i + 1] = v.y;
+                            }
+                            const uint32_t s2 = scale_pair(base[page * F::kDB + tok * 4 + qc] * 0x00010001u);
+                            decode<BITS>(w, s2, offset_pair<BITS>(s2), ka[e]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) sc[i][u][c] = 0.0f;
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_16816(sc[i][u], ka[0][2 * ks], ka[1][2 * ks], ka[0][2 * ks + 1], ka[1][2 * ks + 1],
+                                          qb[i][2 * ks], qb[i][2 * ks + 1]);
+                        }
+                    }
+                    const uint32_t bad = meta[st];
+                    if (key0 + 32 > least || bad) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int kk = 32 * warp + 16 * u + 8 * e + qg, key = t * 128 + kk;
+                                const bool gone = (bad >> (kk >> a.page_log2)) & 1;
+#pragma unroll
+                                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+                                        if (gone || key >= min(lim[i][c], g.sc.len)) sc[i][u][2 * e + c] = -INFINITY;
+                            }
+                    }
+                    // running maximum, raised only when a score is over it by more than 2^8
+                    float mx[NT][2];
+                    bool up = false;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            mx[i][c] = a.scale_log2 * fmaxf(fmaxf(sc[i][0][c], sc[i][0][2 + c]),
+                                                            fmaxf(sc[i][1][c], sc[i][1][2 + c]));
+                            up |= mx[i][c] > m[i][c] + 8.0f;
+                        }
+                    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1)
+                                    mx[i][c] = fmaxf(mx[i][c], __shfl_xor_sync(0xffffffffu, mx[i][c], d));
+                                const float mn = fmaxf(m[i][c], mx[i][c]);
+                                const float alpha = mn == -INFINITY ? 1.0f : ex2_approx(m[i][c] - mn);
+                                m[i][c] = mn;
+                                l[i][c] *= alpha;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    o[i][j][c] *= alpha;
+                                    o[i][j][2 + c] *= alpha;
+                                }
+                            }
+                    }
+                    uint32_t pb[NT][2][2];
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const float m0 = m[i][0] == -INFINITY ? 0.0f : m[i][0];
+                        const float m1 = m[i][1] == -INFINITY ? 0.0f : m[i][1];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float p0 = ex2_approx(fmaf(sc[i][u][2 * e], a.scale_log2, -m0));
+                                const float p1 = ex2_approx(fmaf(sc[i][u][2 * e + 1], a.scale_log2, -m1));
+                                l[i][0] += p0;
+                                l[i][1] += p1;
+                                // P enters its product rounded to bf16, as in the other attention
+                                // kernels; the sum takes it unrounded
+                                pb[i][u][e] = transpose_8x8(pack_bf16x2(p0, p1));
+                            }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int kk = 32 * warp + 16 * u, slot = kk & (page - 1);
+                        const uint8_t* base = ring + (kk >> a.page_log2) * a.page_bytes;
+                        uint32_t va[2][8];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int pair = slot / 2 + 4 * e + qc;
+                            uint32_t w[F::kWords];
+                            const uint2* src = reinterpret_cast<const uint2*>(base + page * (F::kDB + 4) +
+                                                                              pair * (2 * F::kDB) + qg * (F::kDB / 4));
+#pragma unroll
+                            for (int i = 0; i < F::kWords; i += 2) {
+                                const uint2 v = src[i / 2];
+                                w[i] = v.x;
+                                w[i + 1] = v.y;
+                            }
+                            const uint32_t sb = *reinterpret_cast<const uint16_t*>(base + page * (2 * F::kDB + 4) +
+                                                                                   pair * 8 + (qg & ~1));
+                            const uint32_t s2 = scale_pair((sb & 0xFFu) | (sb & 0xFF00u) << 8);
+                            decode<BITS>(w, s2, offset_pair<BITS>(s2), va[e]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                mma_16816(o[i][j], va[0][2 * j], va[0][2 * j + 1], va[1][2 * j], va[1][2 * j + 1],
+                                          pb[i][u][0], pb[i][u][1]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+            }
+            // ---- join the four warps' parts
+            float* mo = reinterpret_cast<float*>(smem + L::kMergeO) + warp * L::kRows * L::kMergeRow;
+            float* ml = reinterpret_cast<float*>(smem + L::kMergeMl) + warp * 2 * L::kRows;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[i][c] += __shfl_xor_sync(0xffffffffu, l[i][c], d);
+                    const int x = 8 * i + 2 * qc + c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float2*>(mo + x * L::kMergeRow + 8 * qg + 2 * j) =
+                            make_float2(o[i][j][c], o[i][j][2 + c]);
+                    if (qg == 0) {
+                        ml[x] = m[i][c];
+                        ml[L::kRows + x] = l[i][c];
+                    }
+                }
+            ok = all_agree(1, 32 * L::kWarps, ok);  // a wait that ran out ends all four warps here
+            const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+            const float* all_ml = reinterpret_cast<const float*>(smem + L::kMergeMl);
+            const float* all_o = reinterpret_cast<const float*>(smem + L::kMergeO);
+            const int slot = part_slot(first_seg);
+            if (ok)
+                for (int x = threadIdx.x / 16; x < nv; x += 8) {
+                    const int c4 = threadIdx.x % 16;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < L::kWarps; ++w) mm = fmaxf(mm, all_ml[w * 2 * L::kRows + x]);
+                    const float mu = mm == -INFINITY ? 0.0f : mm;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < L::kWarps; ++w) {
+                        const float f = ex2_approx(all_ml[w * 2 * L::kRows + x] - mu);
+                        const float4 v =
+                            *reinterpret_cast<const float4*>(all_o + (w * L::kRows + x) * L::kMergeRow + 4 * c4);
+                        acc.x += f * v.x;
+                        acc.y += f * v.y;
+                        acc.z += f * v.z;
+                        acc.w += f * v.w;
+                        sum += f * all_ml[w * 2 * L::kRows + L::kRows + x];
+                    }
+                    if (whole) {
+                        const int64_t row = out_row(a, g.s, g.h, r0 + x);
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
+                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                        if (a.lse && c4 == 0)
+                            a.lse[row] = sum == 0.0f ? -INFINITY : (mu + log2f(sum)) * 0.69314718055994530942f;
+                    } else {
+                        *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * a.tile_rows + x) * 64 + 4 * c4) = acc;
+                        if (c4 == 0) {
+                            a.part_ml[(int64_t)slot * 2 * a.tile_rows + x] = mm;
+                            a.part_ml[((int64_t)slot * 2 + 1) * a.tile_rows + x] = sum;
+                        }
+                    }
+                }
+            first_seg = false;
+            named_bar_sync(1, 32 * L::kWarps);
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------ joining the parts
+//
+// One block per (entry, head, 8 rows): rows of a problem that several CTAs shared, and rows of one
+// that has no keys at all.  Four groups of threads sum every fourth part, in order, then the groups
+// in order.
+constexpr int kMergeThreads = 512;
+
+__global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs a) {
+    __shared__ int64_t red[kMergeThreads / 32];
+    __shared__ int64_t before_smem;
+    __shared__ float4 acc_smem[4][8][16];
+    __shared__ float ml_smem[4][2][8];
+    const int64_t e = blockIdx.x / a.kv_heads;
+    const int h = (int)(blockIdx.x % a.kv_heads);
+    const int s = (int)(e / a.row_tiles), rt = (int)(e % a.row_tiles);
+    const Scene sc = scene_of(a, s);
+    const int32_t nv = valid_rows(a, sc, rt), tiles = key_tiles(a, sc, rt);
+    const int grp = threadIdx.x / 128, x = (threadIdx.x / 16) % 8, c4 = threadIdx.x % 16;
+    const int row_in = 8 * blockIdx.y + x;
+    if (8 * (int)blockIdx.y >= nv || tiles == 0) {
+        if (grp == 0 && row_in < nv) {  // rows that see no key
+            const int64_t row = out_row(a, s, h, (int64_t)rt * a.tile_rows + row_in);
+            *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) = make_uint2(0u, 0u);
+            if (a.lse && c4 == 0) a.lse[row] = -INFINITY;
+        }
+        wait_previous_kernel();
+        return;
+    }
+    const Cut cut = cut_of(a, red);
+    // key tiles before this problem
+    int64_t sum = 0;
+    __syncthreads();
+    for (int64_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_tiles(a, y);
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int64_t b = 0;
+        for (int w = 0; w < kMergeThreads / 32; ++w) b += red[w];
+        before_smem = b + (int64_t)h * tiles;
+    }
+    __syncthreads();
+    const int64_t g0 = before_smem, g1 = g0 + tiles;
+    const int c0 = (int)(g0 / cut.per), c1 = (int)((g1 - 1) / cut.per);
+    wait_previous_kernel();
+    if (c0 == c1) return;  // one CTA had all of it and wrote the rows
+    float m = -INFINITY, l = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row_in < nv) {
+        for (int c = c0 + grp; c <= c1; c += 4) {
+            const int64_t slot = 2 * (int64_t)c + (g0 <= c * cut.per ? 0 : 1);
+            const float pm = __ldcg(a.part_ml + slot * 2 * a.tile_rows + row_in);
+            const float pl = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + row_in);
+            const float4 v =
+                __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + row_in) * 64 + 4 * c4));
+            const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.0f : mn;
+            const float f = ex2_approx(m - mu), w = ex2_approx(pm - mu);
+            acc.x = acc.x * f + v.x * w;
+            acc.y = acc.y * f + v.y * w;
+            acc.z = acc.z * f + v.z * w;
+            acc.w = acc.w * f + v.w * w;
+            l = l * f + pl * w;
+            m = mn;
+        }
+    }
+    acc_smem[grp][x][c4] = acc;
+    if (c4 == 0) ml_smem[grp][0][x] = m, ml_smem[grp][1][x] = l;
+    __syncthreads();
+    if (grp != 0 || row_in >= nv) return;
+    for (int y = 1; y < 4; ++y) m = fmaxf(m, ml_smem[y][0][x]);
+    const float mu = m == -INFINITY ? 0.0f : m;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const float w = ex2_approx(ml_smem[y][0][x] - mu);
+        const float4 v = acc_smem[y][x][c4];
+        acc.x += v.x * w;
+        acc.y += v.y * w;
+        acc.z += v.z * w;
+        acc.w += v.w * w;
+        l += ml_smem[y][1][x] * w;
+    }
+    const int64_t row = out_row(a, s, h, (int64_t)rt * a.tile_rows + row_in);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && c4 == 0) a.lse[row] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994530942f;
+}
+
+}  // namespace kv

@@ -10,6 +10,8 @@
 #include "k_attn_tc.cuh"
 #include "k_attn_tcg.cuh"
 #include "k_budget.cuh"
+#include "k_kv_attn.cuh"
+#include "k_kv_cache.cuh"
 #include "k_pool.cuh"
 #include "k_scores_tc.cuh"
 #include "k_select.cuh"
@@ -564,8 +566,9 @@ const char* sa_status_string(sa_status s) {
         case SA_ERR_UNSUPPORTED: return "unsupported shape or type";
         case SA_ERR_CUDA: return "CUDA error";
         case SA_ERR_TIMEOUT: return "device wait timed out";
-        case SA_ERR_BAD_LIST: return "kept list entry out of range";
+        case SA_ERR_BAD_LIST: return "list or page table entry out of range";
         case SA_ERR_WORKSPACE: return "workspace missing or too small";
+        case SA_ERR_NONFINITE: return "infinities or NaN cannot be stored";
     }
     return "unknown status";
 }
@@ -1322,6 +1325,248 @@ sa_status sa_sparse_attn_bwd(const sa_shape* shape, const void* q, const void* k
         if ((st = launch_status()) != SA_OK) return st;
     }
     return SA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------- the frame cache
+namespace {
+
+struct KvGeo {
+    int64_t page_bytes;
+    int32_t page_log2;
+};
+
+sa_status kv_geo(const sa_kv_cache* c, KvGeo* g) {
+    if (!c) return SA_ERR_INVALID_ARG;
+    if (c->scenes < 1 || c->heads < 1 || c->head_dim < 1 || c->n_pages < 1 || c->max_pages < 1) return SA_ERR_INVALID_ARG;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SA_ERR_INVALID_ARG;
+    if (c->bits != 4 && c->bits != 8) return SA_ERR_INVALID_ARG;
+    if (c->head_dim != 64) return SA_ERR_UNSUPPORTED;
+    if ((int64_t)c->max_pages * c->page > (int64_t(1) << 31) - 256) return SA_ERR_UNSUPPORTED;
+    if ((int64_t)c->scenes * c->heads >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
+    g->page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+    g->page_bytes = (int64_t)c->page * (c->bits == 4 ? kv::Fmt<4>::kTokenBytes : kv::Fmt<8>::kTokenBytes);
+    return SA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Thread blocks of the two row kernels: one column per (scene, head), enough blocks along the rows
+// that every SM has work, each taking 64 token pairs at a time.
+dim3 kv_rows_grid(const sa_kv_cache* c, int32_t n) {
+    const int64_t chunks = ((int64_t)n / 2 + 1 + 63) / 64;
+    return dim3((unsigned)((int64_t)c->scenes * c->heads), (unsigned)std::min<int64_t>(chunks, 65535));
+}
+
+constexpr int kKvMaxCtas = 640;  // largest grid of the attention kernel
+
+// Query rows of one problem: all rows of a key head's query heads together, 32 at most.
+int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+size_t kv_part_bytes(int32_t tile_rows) { return align256((size_t)2 * kKvMaxCtas * tile_rows * 64 * 4); }
+
+sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvGeo* g) {
+    const sa_status st = kv_geo(c, g);
+    if (st != SA_OK) return st;
+    if (q_heads < 1 || q_heads % c->heads != 0 || rows < 1) return SA_ERR_INVALID_ARG;
+    if ((int64_t)c->scenes * q_heads >= (int64_t(1) << 31) || (int64_t)c->scenes * q_heads * rows >= (int64_t(1) << 31))
+        return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+std::mutex g_kv_mu;
+int g_kv_grid[kMaxDevices][2][3];  // resident blocks of each few-rows kernel, per device
+
+template <int BITS, int NT>
+sa_status kv_few_grid(int dev, int* out) {
+    constexpr int kNt = NT == 1 ? 0 : NT == 2 ? 1 : 2;
+    std::lock_guard<std::mutex> lk(g_kv_mu);
+    int& grid = g_kv_grid[dev][BITS == 8][kNt];
+    if (grid == 0) {
+        const int smem = kv::FewLayout<BITS, NT>::smem_bytes();
+        int per_sm = 0;
+        if (cudaFuncSetAttribute(kv::kv_few_rows_kernel<BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv::kv_few_rows_kernel<BITS, NT>,
+                                                          kv::FewLayout<BITS, NT>::kThreads, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return SA_ERR_CUDA;
+        }
+        if (per_sm < 1) return SA_ERR_UNSUPPORTED;
+        grid = std::min(kKvMaxCtas, g_sm_count[dev] * per_sm);
+    }
+    *out = grid;
+    return SA_OK;
+}
+
+template <int BITS, int NT>
+sa_status kv_few_launch(kv::AttnArgs& a, int dev, cudaStream_t stream) {
+    const sa_status st = kv_few_grid<BITS, NT>(dev, &a.ctas);
+    if (st != SA_OK) return st;
+    using L = kv::FewLayout<BITS, NT>;
+    kv::kv_few_rows_kernel<BITS, NT><<<a.ctas, L::kThreads, L::smem_bytes(), stream>>>(a);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sa_kv_pool_size(const sa_kv_cache* cache) {
+    KvGeo g;
+    if (kv_geo(cache, &g) != SA_OK) return 0;
+    return (size_t)cache->n_pages * cache->heads * g.page_bytes;
+}
+
+sa_status sa_kv_append(const sa_kv_cache* cache, sa_dtype dtype, const void* k, const void* v, int32_t n,
+                       const int32_t* n_len_or_null, const int32_t* lens, const int32_t* page_table, void* pool,
+                       sa_stream_t stream) {
+    KvGeo g;
+    sa_status st = kv_geo(cache, &g);
+    if (st != SA_OK) return st;
+    if (dtype != SA_F32 && dtype != SA_BF16) return SA_ERR_INVALID_ARG;
+    if (n < 1 || !k || !v || !lens || !page_table || !pool) return SA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(pool) || !aligned4(lens) || !aligned4(page_table) ||
+        !aligned4(n_len_or_null))
+        return SA_ERR_INVALID_ARG;
+    kv::CacheArgs a;
+    memset(&a, 0, sizeof(a));
+    a.pool = static_cast<uint8_t*>(pool);
+    a.table = page_table;
+    a.lens = lens;
+    a.n_len = n_len_or_null;
+    a.k = const_cast<void*>(k);
+    a.v = const_cast<void*>(v);
+    a.scenes = cache->scenes;
+    a.heads = cache->heads;
+    a.n = n;
+    a.page_log2 = g.page_log2;
+    a.n_pages = cache->n_pages;
+    a.max_pages = cache->max_pages;
+    a.page_bytes = g.page_bytes;
+    const dim3 grid = kv_rows_grid(cache, n);
+    if (cache->bits == 4)
+        dtype == SA_BF16 ? kv::append_kernel<4, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
+                         : kv::append_kernel<4, float><<<grid, 256, 0, stream>>>(a);
+    else
+        dtype == SA_BF16 ? kv::append_kernel<8, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
+                         : kv::append_kernel<8, float><<<grid, 256, 0, stream>>>(a);
+    return launch_status();
+}
+
+sa_status sa_kv_read(const sa_kv_cache* cache, sa_dtype dtype, int32_t n, const int32_t* n_len_or_null,
+                     const int32_t* start_or_null, const int32_t* lens, const int32_t* page_table, const void* pool,
+                     void* k_or_null, void* v_or_null, sa_stream_t stream) {
+    KvGeo g;
+    sa_status st = kv_geo(cache, &g);
+    if (st != SA_OK) return st;
+    if (dtype != SA_F32 && dtype != SA_BF16) return SA_ERR_INVALID_ARG;
+    if (n < 1 || (!k_or_null && !v_or_null) || !lens || !page_table || !pool) return SA_ERR_INVALID_ARG;
+    if (!aligned16(k_or_null) || !aligned16(v_or_null) || !aligned16(pool) || !aligned4(lens) ||
+        !aligned4(page_table) || !aligned4(n_len_or_null) || !aligned4(start_or_null))
+        return SA_ERR_INVALID_ARG;
+    kv::CacheArgs a;
+    memset(&a, 0, sizeof(a));
+    a.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+    a.table = page_table;
+    a.lens = lens;
+    a.n_len = n_len_or_null;
+    a.start = start_or_null;
+    a.k = k_or_null;
+    a.v = v_or_null;
+    a.scenes = cache->scenes;
+    a.heads = cache->heads;
+    a.n = n;
+    a.page_log2 = g.page_log2;
+    a.n_pages = cache->n_pages;
+    a.max_pages = cache->max_pages;
+    a.page_bytes = g.page_bytes;
+    const dim3 grid = kv_rows_grid(cache, n);
+    if (cache->bits == 4)
+        dtype == SA_BF16 ? kv::read_kernel<4, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
+                         : kv::read_kernel<4, float><<<grid, 256, 0, stream>>>(a);
+    else
+        dtype == SA_BF16 ? kv::read_kernel<8, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
+                         : kv::read_kernel<8, float><<<grid, 256, 0, stream>>>(a);
+    return launch_status();
+}
+
+size_t sa_kv_attn_workspace_size(const sa_kv_cache* cache, int32_t q_heads, int32_t rows) {
+    KvGeo g;
+    if (kv_attn_check(cache, q_heads, rows, &g) != SA_OK) return 0;
+    const int32_t tr = kv_tile_rows((int64_t)rows * (q_heads / cache->heads));
+    return kv_part_bytes(tr) + align256((size_t)2 * kKvMaxCtas * 2 * tr * 4);
+}
+
+sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_heads, int32_t rows,
+                         const int32_t* q_len_or_null, int32_t frame, float softmax_scale, const int32_t* lens,
+                         const int32_t* page_table, const void* pool, void* workspace, size_t workspace_bytes,
+                         void* o, float* lse_or_null, sa_stream_t stream) {
+    KvGeo g;
+    sa_status st = kv_attn_check(cache, q_heads, rows, &g);
+    if (st != SA_OK) return st;
+    if (frame < 0 || !(softmax_scale >= 0.0f) || isinf(softmax_scale)) return SA_ERR_INVALID_ARG;
+    if (!q || !lens || !page_table || !pool || !o) return SA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(pool) || !aligned16(o) || !aligned16(workspace) || !aligned4(lens) ||
+        !aligned4(page_table) || !aligned4(q_len_or_null) || !aligned4(lse_or_null))
+        return SA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < sa_kv_attn_workspace_size(cache, q_heads, rows)) return SA_ERR_WORKSPACE;
+    if ((st = ensure_attributes()) != SA_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
+    kv::AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    a.pool = static_cast<const uint8_t*>(pool);
+    a.table = page_table;
+    a.lens = lens;
+    a.q_len = q_len_or_null;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse_or_null;
+    a.scenes = cache->scenes;
+    a.kv_heads = cache->heads;
+    a.group = q_heads / cache->heads;
+    a.rows = rows;
+    const int64_t head_rows = (int64_t)rows * a.group;
+    a.tile_rows = kv_tile_rows(head_rows);
+    a.row_tiles = (int32_t)((head_rows + a.tile_rows - 1) / a.tile_rows);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv_part_bytes(a.tile_rows));
+    a.page_log2 = g.page_log2;
+    a.n_pages = cache->n_pages;
+    a.max_pages = cache->max_pages;
+    a.frame = frame;
+    a.min_tiles = 1;
+    a.page_bytes = g.page_bytes;
+    const float scale = softmax_scale > 0.0f ? softmax_scale : 0.125f;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    const int64_t problems = (int64_t)a.scenes * a.row_tiles * a.kv_heads;
+    if (problems >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
+    const bool b4 = cache->bits == 4;
+    if (a.tile_rows == 8)
+        st = b4 ? kv_few_launch<4, 1>(a, dev, stream) : kv_few_launch<8, 1>(a, dev, stream);
+    else if (a.tile_rows == 16)
+        st = b4 ? kv_few_launch<4, 2>(a, dev, stream) : kv_few_launch<8, 2>(a, dev, stream);
+    else
+        st = b4 ? kv_few_launch<4, 4>(a, dev, stream) : kv_few_launch<8, 4>(a, dev, stream);
+    if (st != SA_OK) return st;
+    // the joining kernel is launched ahead of the attention kernel's end and waits for it itself
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)problems, (unsigned)(a.tile_rows / 8));
+    cfg.blockDim = dim3(kv::kMergeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kv::kv_merge_kernel, (const kv::AttnArgs)a) != cudaSuccess) {
+        cudaGetLastError();
+        return SA_ERR_CUDA;
+    }
+    return launch_status();
 }
 
 }  // extern "C"

@@ -341,3 +341,222 @@ class DenseAttention:
     def __call__(self, q, k, v, stream=None):
         sa.sa_dense_attn_fwd(self.shape, q, k, v, self.ws, self.o, self.lse, stream)
         return self.o, self.lse
+
+
+def _want(name, t, shape, dtypes, device):
+    """Refuse a tensor that is not of this shape, one of these types, contiguous and on this device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s has type %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
+    if t.device != device:
+        raise ValueError("%s is on %s, the cache is on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s is not contiguous" % name)
+    if t.data_ptr() % (16 if t.dtype != _int32() else 4):
+        raise ValueError("%s does not start on a 16-byte boundary" % name)
+
+
+def _int32():
+    import torch
+    return torch.int32
+
+
+class FrameCache:
+    """K and V of the frames seen so far, of one layer, held in 4 or 8 bits in pages.
+
+    scenes     independent scenes of any lengths
+    heads      key/value heads
+    tokens     the longest scene, in tokens
+    n_pages    pages of the pool, shared by the scenes (default: enough for every scene at its longest)
+    page       tokens per page (16, 32, 64 or 128)
+    bits       4 (72 bytes per token and head for K and V) or 8 (136 bytes)
+
+    `grow(n)` counts new tokens in and gives them pages; `append(k, v)` then writes their rows;
+    `read` hands rows back; `CachedGlobalAttention` attends over them.  Lengths (`lens`) and page
+    table (`page_table`) are device tensors read by the kernels when they run, so recorded graphs
+    follow them.  The layers of a model see the same tokens: give the second and later layers'
+    caches `like=` the first one and they share its lengths, its table and its pages' numbering
+    (and only the first one's grow and release are called).  `wrap` adopts tensors that the caller
+    manages.  Calls on one cache are ordered by the caller (one stream, or events).
+    """
+
+    def __init__(self, scenes: int, heads: int, tokens: int, n_pages: int | None = None, page: int = 128, bits: int = 4,
+                 head_dim: int = 64, device=None, like: "FrameCache | None" = None):
+        import torch
+        if page not in (16, 32, 64, 128):
+            raise ValueError("page is 16, 32, 64 or 128 tokens")
+        max_pages = -(-int(tokens) // page)
+        if like is not None:
+            if (like.scenes, like.page, like.max_pages) != (scenes, page, max_pages) or n_pages not in (None, like.n_pages):
+                raise ValueError("a cache like another has its scenes, page size, length and pages")
+            n_pages, device = like.n_pages, like.device
+        n_pages = scenes * max_pages if n_pages is None else int(n_pages)
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self._describe(scenes, heads, n_pages, max_pages, page, bits, head_dim, dev)
+        self.pool = torch.empty((self.pool_bytes,), dtype=torch.uint8, device=dev)
+        self._owner = like is None
+        if like is not None:
+            self.page_table, self.lens = like.page_table, like.lens
+            return
+        self.page_table = torch.full((scenes, max_pages), -1, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros((scenes,), dtype=torch.int32, device=dev)
+        self._len = [0] * scenes              # host copies: the pages' bookkeeping is the host's
+        self._pages = [[] for _ in range(scenes)]
+        self._free = list(range(n_pages - 1, -1, -1))
+
+    def _describe(self, scenes, heads, n_pages, max_pages, page, bits, head_dim, device):
+        self.desc = sa.kv_cache(scenes, heads, n_pages, max_pages, page, bits, head_dim)
+        self.pool_bytes = sa.sa_kv_pool_size(self.desc)
+        if self.pool_bytes == 0:
+            raise ValueError("unsupported cache (head_dim 64, 4 or 8 bits, at least one scene, head and page)")
+        self.scenes, self.heads, self.n_pages, self.max_pages = scenes, heads, n_pages, max_pages
+        self.page, self.bits, self.d, self.device = page, bits, head_dim, device
+
+    @classmethod
+    def wrap(cls, pool, page_table, lens, page: int = 128, bits: int = 4, head_dim: int = 64) -> "FrameCache":
+        """A cache over the caller's own tensors: pool uint8 [n_pages][heads][bytes of a page], page_table int32
+        [scenes][max_pages], lens int32 [scenes].  The caller assigns pages and sets lengths."""
+        import torch
+        if pool.dim() != 3 or page_table.dim() != 2:
+            raise ValueError("pool is [n_pages][heads][bytes], page_table [scenes][max_pages]")
+        c = cls.__new__(cls)
+        c._describe(page_table.shape[0], pool.shape[1], pool.shape[0], page_table.shape[1], page, bits, head_dim,
+                    pool.device)
+        per_page = c.pool_bytes // (c.n_pages * c.heads)
+        _want("pool", pool, (c.n_pages, c.heads, per_page), (torch.uint8,), pool.device)
+        _want("page_table", page_table, (c.scenes, c.max_pages), (torch.int32,), pool.device)
+        _want("lens", lens, (c.scenes,), (torch.int32,), pool.device)
+        c.pool, c.page_table, c.lens, c._owner = pool, page_table, lens, False
+        return c
+
+    # ---- pages and lengths (host bookkeeping, device tables)
+    def _owned(self):
+        if not self._owner:
+            raise ValueError("pages and lengths of this cache are managed elsewhere")
+
+    def grow(self, n):
+        """Count n more tokens (one number, or one per scene) into the cache and give them pages.  Call it once
+        before the layers' appends.  Raises MemoryError, changing nothing, when pages run out."""
+        import torch
+        self._owned()
+        ns = [int(n)] * self.scenes if isinstance(n, int) else [int(x) for x in n]
+        if len(ns) != self.scenes or min(ns) < 0:
+            raise ValueError("grow needs one non-negative count, or one per scene")
+        need = [-(-(self._len[s] + ns[s]) // self.page) for s in range(self.scenes)]
+        if max(need) > self.max_pages:
+            raise ValueError("a scene is longer than its row of the page table")
+        more = [need[s] - len(self._pages[s]) for s in range(self.scenes)]
+        if sum(more) > len(self._free):
+            raise MemoryError("%d more pages needed, %d free" % (sum(more), len(self._free)))
+        rows, cols, ids = [], [], []
+        for s in range(self.scenes):
+            for _ in range(more[s]):
+                rows.append(s)
+                cols.append(len(self._pages[s]))
+                ids.append(self._free.pop())
+                self._pages[s].append(ids[-1])
+            self._len[s] += ns[s]
+        if ids:
+            at = torch.tensor([rows, cols, ids], dtype=torch.int64).to(self.device)
+            self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
+        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+
+    def release(self, scene: int):
+        """Drop a scene: its pages are free again and its length is 0."""
+        import torch
+        self._owned()
+        self._free.extend(reversed(self._pages[scene]))
+        self._pages[scene] = []
+        self._len[scene] = 0
+        self.page_table[scene].fill_(-1)
+        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+
+    # ---- rows (each one C call)
+    def _rows(self, name, t, shape, dtypes):
+        _want(name, t, shape, dtypes, self.device)
+
+    def _counts(self, name, t):
+        if t is not None:
+            import torch
+            _want(name, t, (self.scenes,), (torch.int32,), self.device)
+
+    def append(self, k, v, new_len=None, stream=None):
+        """Write rows k, v [scenes * heads][n][64] (bf16 or f32) as the last n tokens of every scene; with
+        new_len (int32 device tensor [scenes]) only the first new_len[s] rows, as the last new_len[s] tokens."""
+        import torch
+        shape = (self.scenes * self.heads, k.shape[1] if k.dim() == 3 else -1, self.d)
+        self._rows("k", k, shape, (torch.bfloat16, torch.float32))
+        self._rows("v", v, shape, (k.dtype,))
+        self._counts("new_len", new_len)
+        with torch.cuda.device(self.device):
+            sa.sa_kv_append(self.desc, k, v, shape[1], new_len, self.lens, self.page_table, self.pool, stream)
+
+    def read(self, k=None, v=None, start=None, n_len=None, stream=None):
+        """Fill k and v [scenes * heads][n][64] (bf16 or f32, either may be None) with the tokens from start[s]
+        (default: the last n, or n_len[s], of each scene); returns (k, v)."""
+        import torch
+        ref = k if k is not None else v
+        if ref is None:
+            raise ValueError("nothing to read into")
+        shape = (self.scenes * self.heads, ref.shape[1] if ref.dim() == 3 else -1, self.d)
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                self._rows(name, t, shape, (torch.bfloat16, torch.float32) if t is ref else (ref.dtype,))
+        self._counts("start", start)
+        self._counts("n_len", n_len)
+        with torch.cuda.device(self.device):
+            sa.sa_kv_read(self.desc, shape[1], n_len, start, self.lens, self.page_table, self.pool, k, v, stream)
+        return k, v
+
+
+class CachedGlobalAttention:
+    """Attention of up to `rows` query rows per scene over a FrameCache.
+
+    q_heads    query heads (default: the cache's heads; a multiple of them for grouped heads)
+    frame      0: every row sees every cached token; n > 0: the rows are the scene's last tokens and see
+               their own and earlier frames of n tokens (1: causal by token)
+
+    Workspace and outputs are allocated once: an object's calls (and graphs recorded from it) run one
+    after another; calls that overlap need an object each."""
+
+    def __init__(self, cache: FrameCache, rows: int, q_heads: int | None = None, frame: int = 0,
+                 softmax_scale: float = 0.0, with_lse: bool = True):
+        import torch
+        self.cache, self.rows, self.frame = cache, int(rows), int(frame)
+        self.q_heads = cache.heads if q_heads is None else int(q_heads)
+        self.softmax_scale = float(softmax_scale)
+        nbytes = sa.sa_kv_attn_workspace_size(cache.desc, self.q_heads, self.rows)
+        if nbytes == 0:
+            raise ValueError("q_heads is a multiple of the cache's heads and rows is positive")
+        bh, dev = cache.scenes * self.q_heads, cache.device
+        self.ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        self.o = torch.zeros((bh, self.rows, cache.d), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros((bh, self.rows), dtype=torch.float32, device=dev) if with_lse else None
+
+    def forward(self, q, q_len=None, stream=None):
+        """q [scenes * q_heads][rows][64] bf16; with q_len (int32 device tensor [scenes]) only the first q_len[s]
+        rows of scene s.  Returns the (O, LSE) buffers; rows past q_len[s] keep what they held."""
+        import torch
+        c = self.cache
+        _want("q", q, (c.scenes * self.q_heads, self.rows, c.d), (torch.bfloat16,), c.device)
+        c._counts("q_len", q_len)
+        with torch.cuda.device(c.device):
+            sa.sa_kv_attn_fwd(c.desc, q, self.q_heads, self.rows, q_len, self.frame, self.softmax_scale, c.lens,
+                              c.page_table, c.pool, self.ws, self.o, self.lse, stream)
+        return self.o, self.lse
+
+    __call__ = forward
+
+    def capture(self, q, q_len=None):
+        """Record one call on these tensors as a CUDA graph.  A replay follows the cache's lengths and page
+        table as they are then (frames appended in between are seen) and new queries written into q."""
+        import torch
+        self.forward(q, q_len)
+        torch.cuda.current_stream(self.cache.device).synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self.forward(q, q_len)
+        return g

@@ -21,6 +21,7 @@ SA_ERR_CUDA = 3
 SA_ERR_TIMEOUT = 4
 SA_ERR_BAD_LIST = 5
 SA_ERR_WORKSPACE = 6
+SA_ERR_NONFINITE = 7
 
 SA_F32 = 0
 SA_BF16 = 1
@@ -32,6 +33,7 @@ EXPORTS = [
     "sa_head_budgets", "sa_sparse_attn_workspace_size", "sa_sparse_attn_fwd", "sa_dense_attn_workspace_size",
     "sa_dense_attn_fwd", "sa_sga_workspace_size", "sa_sga_fwd", "sa_sparse_attn_bwd_workspace_size",
     "sa_sparse_attn_bwd",
+    "sa_kv_pool_size", "sa_kv_append", "sa_kv_read", "sa_kv_attn_workspace_size", "sa_kv_attn_fwd",
     "sa_status_string", "sa_check_device_error", "sa_set_wait_limit_ns", "sa_test_withhold_query_load",
 ]
 
@@ -46,6 +48,18 @@ class SaShape(ctypes.Structure):
         ("n_sink", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
         ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class SaKvCache(ctypes.Structure):
+    _fields_ = [
+        ("scenes", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("bits", ctypes.c_int32),
     ]
 
 
@@ -69,6 +83,7 @@ def load(path: str | None = None):
     lib = ctypes.CDLL(p)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     shp = ctypes.POINTER(SaShape)
+    kvc = ctypes.POINTER(SaKvCache)
     sig = {
         "sa_num_tiles": (i32, [shp]),
         "sa_max_kept": (i32, [shp, i32]),
@@ -94,6 +109,11 @@ def load(path: str | None = None):
         "sa_sparse_attn_bwd_workspace_size": (sz, [shp, i32, i32]),
         "sa_sparse_attn_bwd": (i32, [shp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, sz, vp,
                                      vp, vp, vp]),
+        "sa_kv_pool_size": (sz, [kvc]),
+        "sa_kv_append": (i32, [kvc, i32, vp, vp, i32, vp, vp, vp, vp, vp]),
+        "sa_kv_read": (i32, [kvc, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "sa_kv_attn_workspace_size": (sz, [kvc, i32, i32]),
+        "sa_kv_attn_fwd": (i32, [kvc, vp, i32, i32, vp, i32, ctypes.c_float, vp, vp, vp, vp, sz, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -261,3 +281,56 @@ def sa_sga_fwd(shp, grid_h, grid_w, s_h, s_w, q, k, v, workspace, o, lse=None, s
     st = load().sa_sga_fwd(ctypes.byref(shp), int(grid_h), int(grid_w), int(s_h), int(s_w), _ptr(q), _ptr(k),
                            _ptr(v), _ptr(workspace), ws_bytes, _ptr(o), _ptr(lse), _stream(stream))
     _check("sa_sga_fwd", st)
+
+
+# ------------------------------------------------------------------------- the frame cache
+
+
+def kv_cache(scenes, heads, n_pages, max_pages, page=128, bits=4, head_dim=64) -> SaKvCache:
+    return SaKvCache(int(scenes), int(heads), int(head_dim), int(page), int(n_pages), int(max_pages), int(bits))
+
+
+def _dtype_of(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return SA_BF16
+    if t.dtype == torch.float32:
+        return SA_F32
+    raise ValueError("expected a bf16 or f32 tensor")
+
+
+def sa_kv_pool_size(cache: SaKvCache) -> int:
+    return int(load().sa_kv_pool_size(ctypes.byref(cache)))
+
+
+def sa_kv_append(cache, k, v, n, n_len, lens, page_table, pool, stream=None):
+    """k, v: [scenes * heads][n][64], both bf16 or both f32; n_len: int32 device tensor [scenes] or None."""
+    if k.dtype != v.dtype:
+        raise ValueError("k and v differ in type")
+    st = load().sa_kv_append(ctypes.byref(cache), _dtype_of(k), _ptr(k), _ptr(v), int(n), _ptr(n_len), _ptr(lens),
+                             _ptr(page_table), _ptr(pool), _stream(stream))
+    _check("sa_kv_append", st)
+
+
+def sa_kv_read(cache, n, n_len, start, lens, page_table, pool, k, v, stream=None):
+    """k, v: outputs [scenes * heads][n][64] (one of them may be None); start: int32 device tensor [scenes] or None."""
+    if k is None and v is None:
+        raise ValueError("nothing to read into")
+    if k is not None and v is not None and k.dtype != v.dtype:
+        raise ValueError("k and v differ in type")
+    st = load().sa_kv_read(ctypes.byref(cache), _dtype_of(k if k is not None else v), int(n), _ptr(n_len), _ptr(start),
+                           _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(k), _ptr(v), _stream(stream))
+    _check("sa_kv_read", st)
+
+
+def sa_kv_attn_workspace_size(cache, q_heads, rows) -> int:
+    return int(load().sa_kv_attn_workspace_size(ctypes.byref(cache), int(q_heads), int(rows)))
+
+
+def sa_kv_attn_fwd(cache, q, q_heads, rows, q_len, frame, softmax_scale, lens, page_table, pool, workspace, o, lse=None,
+                   stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load().sa_kv_attn_fwd(ctypes.byref(cache), _ptr(q), int(q_heads), int(rows), _ptr(q_len), int(frame),
+                               float(softmax_scale), _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(workspace),
+                               ws_bytes, _ptr(o), _ptr(lse), _stream(stream))
+    _check("sa_kv_attn_fwd", st)
