@@ -71,25 +71,25 @@ __device__ __forceinline__ uint32_t offset_pair(uint32_t s2) {
     return hmul2_bf16(s2, BITS == 4 ? 0xC308C308u : 0xC300C300u);  // -136, -128
 }
 
-// Decodes the words of 16 code pairs' halves: out[p] holds (low unit's code p, high unit's code p)
-// times their scales.  One mask and one FMA a pair (plus a shift, or a byte swap and the sign).
+// Decodes one word: out[p] holds (low unit's code p, high unit's code p) times their scales.  One
+// mask and one FMA a pair (plus a shift, or a byte swap and the sign).
+template <int BITS>
+__device__ __forceinline__ void decode_word(uint32_t x, uint32_t s2, uint32_t c2, uint32_t* out) {
+    if constexpr (BITS == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[j] = hfma2_bf16(and_or(x >> (4 * j), 0x000F000Fu, 0x43004300u), s2, c2);
+    } else {
+        const uint32_t y = __byte_perm(x, 0, 0x2301);
+        out[0] = hfma2_bf16(and_or(x, 0x807F807Fu, 0x43004300u), s2, and_xor(x, 0x80008000u, c2));
+        out[1] = hfma2_bf16(and_or(y, 0x807F807Fu, 0x43004300u), s2, and_xor(y, 0x80008000u, c2));
+    }
+}
+// The words of 16 codes (a K block, or 8 channels of a V pair), in order.
 template <int BITS>
 __device__ __forceinline__ void decode(const uint32_t (&w)[Fmt<BITS>::kWords], uint32_t s2, uint32_t c2,
                                        uint32_t (&out)[8]) {
-    if constexpr (BITS == 4) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                out[4 * i + j] = hfma2_bf16(and_or(w[i] >> (4 * j), 0x000F000Fu, 0x43004300u), s2, c2);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t x = w[i], y = __byte_perm(w[i], 0, 0x2301);
-            out[2 * i] = hfma2_bf16(and_or(x, 0x807F807Fu, 0x43004300u), s2, and_xor(x, 0x80008000u, c2));
-            out[2 * i + 1] = hfma2_bf16(and_or(y, 0x807F807Fu, 0x43004300u), s2, and_xor(y, 0x80008000u, c2));
-        }
-    }
+    for (int i = 0; i < Fmt<BITS>::kWords; ++i) decode_word<BITS>(w[i], s2, c2, out + i * (16 / BITS));
 }
 
 struct CacheArgs {

@@ -11,6 +11,7 @@
 #include "k_attn_tcg.cuh"
 #include "k_budget.cuh"
 #include "k_kv_attn.cuh"
+#include "k_kv_attn_tc.cuh"
 #include "k_kv_cache.cuh"
 #include "k_pool.cuh"
 #include "k_scores_tc.cuh"
@@ -1359,12 +1360,16 @@ dim3 kv_rows_grid(const sa_kv_cache* c, int32_t n) {
     return dim3((unsigned)((int64_t)c->scenes * c->heads), (unsigned)std::min<int64_t>(chunks, 65535));
 }
 
-constexpr int kKvMaxCtas = 640;  // largest grid of the attention kernel
+// Query rows of one problem: all rows of a key head's query heads together, in the smallest tile of
+// the few-rows kernel, or 128 at a time on the tensor cores.
+int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
-// Query rows of one problem: all rows of a key head's query heads together, 32 at most.
-int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// Largest grids of the attention kernels: what the workspace has room for.
+int kv_max_ctas(int32_t tile_rows) { return tile_rows == 128 ? 320 : 640; }
 
-size_t kv_part_bytes(int32_t tile_rows) { return align256((size_t)2 * kKvMaxCtas * tile_rows * 64 * 4); }
+size_t kv_part_bytes(int32_t tile_rows) {
+    return align256((size_t)2 * kv_max_ctas(tile_rows) * tile_rows * 64 * 4);
+}
 
 sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvGeo* g) {
     const sa_status st = kv_geo(c, g);
@@ -1376,37 +1381,56 @@ sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvG
 }
 
 std::mutex g_kv_mu;
-int g_kv_grid[kMaxDevices][2][3];  // resident blocks of each few-rows kernel, per device
+int g_kv_grid[kMaxDevices][2][4];  // resident blocks of each attention kernel, per device
 
-template <int BITS, int NT>
-sa_status kv_few_grid(int dev, int* out) {
-    constexpr int kNt = NT == 1 ? 0 : NT == 2 ? 1 : 2;
-    std::lock_guard<std::mutex> lk(g_kv_mu);
-    int& grid = g_kv_grid[dev][BITS == 8][kNt];
-    if (grid == 0) {
-        const int smem = kv::FewLayout<BITS, NT>::smem_bytes();
-        int per_sm = 0;
-        if (cudaFuncSetAttribute(kv::kv_few_rows_kernel<BITS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kv::kv_few_rows_kernel<BITS, NT>,
-                                                          kv::FewLayout<BITS, NT>::kThreads, smem) != cudaSuccess) {
-            cudaGetLastError();
-            return SA_ERR_CUDA;
+// Launches an attention kernel with as many blocks as stay resident (each takes an equal run of
+// key tiles); `which` names the kernel's place in g_kv_grid.
+sa_status kv_launch(void (*kernel)(const kv::AttnArgs), kv::AttnArgs& a, int dev, int bits, int which, int threads,
+                    int smem, cudaStream_t stream) {
+    {
+        std::lock_guard<std::mutex> lk(g_kv_mu);
+        int& grid = g_kv_grid[dev][bits == 8][which];
+        if (grid == 0) {
+            int per_sm = 0;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess) {
+                cudaGetLastError();
+                return SA_ERR_CUDA;
+            }
+            if (per_sm < 1) return SA_ERR_UNSUPPORTED;
+            if (which == 3) {
+                // two blocks fit an SM by design (registers, shared memory and all of the tensor memory);
+                // the register split needs what it hands out
+                per_sm = 2;
+                cudaFuncAttributes fa;
+                if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
+                    cudaGetLastError();
+                    return SA_ERR_CUDA;
+                }
+                if ((uint32_t)fa.numRegs * (uint32_t)threads < kv::TcLayoutKv::kRegsNeeded) return SA_ERR_UNSUPPORTED;
+            }
+            grid = std::min(kv_max_ctas(a.tile_rows), g_sm_count[dev] * per_sm);
         }
-        if (per_sm < 1) return SA_ERR_UNSUPPORTED;
-        grid = std::min(kKvMaxCtas, g_sm_count[dev] * per_sm);
+        a.ctas = grid;
     }
-    *out = grid;
-    return SA_OK;
+    kernel<<<a.ctas, threads, smem, stream>>>(a);
+    return launch_status();
 }
 
-template <int BITS, int NT>
-sa_status kv_few_launch(kv::AttnArgs& a, int dev, cudaStream_t stream) {
-    const sa_status st = kv_few_grid<BITS, NT>(dev, &a.ctas);
-    if (st != SA_OK) return st;
-    using L = kv::FewLayout<BITS, NT>;
-    kv::kv_few_rows_kernel<BITS, NT><<<a.ctas, L::kThreads, L::smem_bytes(), stream>>>(a);
-    return launch_status();
+template <int BITS>
+sa_status kv_launch_rows(kv::AttnArgs& a, int dev, cudaStream_t stream) {
+    using kv::FewLayout;
+    if (a.tile_rows == 8)
+        return kv_launch(kv::kv_few_rows_kernel<BITS, 1>, a, dev, BITS, 0, FewLayout<BITS, 1>::kThreads,
+                         FewLayout<BITS, 1>::smem_bytes(), stream);
+    if (a.tile_rows == 16)
+        return kv_launch(kv::kv_few_rows_kernel<BITS, 2>, a, dev, BITS, 1, FewLayout<BITS, 2>::kThreads,
+                         FewLayout<BITS, 2>::smem_bytes(), stream);
+    if (a.tile_rows == 32)
+        return kv_launch(kv::kv_few_rows_kernel<BITS, 4>, a, dev, BITS, 2, FewLayout<BITS, 4>::kThreads,
+                         FewLayout<BITS, 4>::smem_bytes(), stream);
+    return kv_launch(kv::kv_tc_kernel<BITS>, a, dev, BITS, 3, kv::TcLayoutKv::kThreads, kv::TcLayoutKv::smem_bytes(),
+                     stream);
 }
 
 }  // namespace
@@ -1496,7 +1520,7 @@ size_t sa_kv_attn_workspace_size(const sa_kv_cache* cache, int32_t q_heads, int3
     KvGeo g;
     if (kv_attn_check(cache, q_heads, rows, &g) != SA_OK) return 0;
     const int32_t tr = kv_tile_rows((int64_t)rows * (q_heads / cache->heads));
-    return kv_part_bytes(tr) + align256((size_t)2 * kKvMaxCtas * 2 * tr * 4);
+    return kv_part_bytes(tr) + align256((size_t)2 * kv_max_ctas(tr) * 2 * tr * 4);
 }
 
 sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_heads, int32_t rows,
@@ -1543,14 +1567,8 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int64_t problems = (int64_t)a.scenes * a.row_tiles * a.kv_heads;
     if (problems >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
-    const bool b4 = cache->bits == 4;
-    if (a.tile_rows == 8)
-        st = b4 ? kv_few_launch<4, 1>(a, dev, stream) : kv_few_launch<8, 1>(a, dev, stream);
-    else if (a.tile_rows == 16)
-        st = b4 ? kv_few_launch<4, 2>(a, dev, stream) : kv_few_launch<8, 2>(a, dev, stream);
-    else
-        st = b4 ? kv_few_launch<4, 4>(a, dev, stream) : kv_few_launch<8, 4>(a, dev, stream);
-    if (st != SA_OK) return st;
+    if ((st = cache->bits == 4 ? kv_launch_rows<4>(a, dev, stream) : kv_launch_rows<8>(a, dev, stream)) != SA_OK)
+        return st;
     // the joining kernel is launched ahead of the attention kernel's end and waits for it itself
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
