@@ -48,16 +48,17 @@ __device__ __forceinline__ int32_t key_limit(const AttnArgs& a, const Scene& sc,
 // A problem's rows are numbered row-major, the query heads of one key head innermost: row x of the
 // (scene, key head) is query row x / group of query head x % group.  Limits ascend with x.
 __device__ __forceinline__ int32_t valid_rows(const AttnArgs& a, const Scene& sc, int32_t rt) {
-    return max(0, (int32_t)min((int64_t)a.tile_rows, (int64_t)sc.n * a.group - (int64_t)rt * a.tile_rows));
+    return max(0, min(a.tile_rows, sc.n * a.group - rt * a.tile_rows));
 }
 __device__ __forceinline__ int32_t key_tiles(const AttnArgs& a, const Scene& sc, int32_t rt) {
     const int32_t nv = valid_rows(a, sc, rt);
     if (nv == 0) return 0;
-    return (int32_t)(((int64_t)key_limit(a, sc, (int32_t)(((int64_t)rt * a.tile_rows + nv - 1) / a.group)) + 127) / 128);
+    return (key_limit(a, sc, (rt * a.tile_rows + nv - 1) / a.group) + 127) / 128;
 }
-__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int s, int h, int64_t x) {
-    const int64_t head = ((int64_t)s * a.kv_heads + h) * a.group + x % a.group;
-    return head * a.rows + x / a.group;
+// (rows * group, scenes * row_tiles and the rows of all heads are below 2^31: checked on the host)
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, int s, int h, int32_t x) {
+    const int32_t r = x / a.group;
+    return (int64_t)((s * a.kv_heads + h) * a.group + (x - r * a.group)) * a.rows + r;
 }
 
 // Named barrier over `nthreads` threads that tells each of them whether all came with true.
@@ -88,15 +89,15 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-__device__ __forceinline__ int64_t entry_tiles(const AttnArgs& a, int64_t e) {
-    const int s = (int)(e / a.row_tiles), rt = (int)(e % a.row_tiles);
-    return (int64_t)key_tiles(a, scene_of(a, s), rt) * a.kv_heads;
+__device__ __forceinline__ int64_t entry_tiles(const AttnArgs& a, int32_t e) {
+    const int s = e / a.row_tiles;
+    return (int64_t)key_tiles(a, scene_of(a, s), e - s * a.row_tiles) * a.kv_heads;
 }
 // Every warp of the block calls it; `red` is shared memory of one int64 per warp.
 __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int64_t* red) {
-    const int64_t n = (int64_t)a.scenes * a.row_tiles;
+    const int32_t n = a.scenes * a.row_tiles;
     int64_t sum = 0;
-    for (int64_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_tiles(a, e);
+    for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_tiles(a, e);
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -105,11 +106,11 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int64_t* red) {
     return Cut{sum, max((sum + a.ctas - 1) / a.ctas, (int64_t)a.min_tiles)};
 }
 // The entry that holds key tile x of the list (x < total), and the tile's index within it.  One warp.
-__device__ __forceinline__ int64_t find_entry(const AttnArgs& a, int64_t x, int64_t* within) {
+__device__ __forceinline__ int32_t find_entry(const AttnArgs& a, int64_t x, int64_t* within) {
     const int lane = threadIdx.x & 31;
-    const int64_t n = (int64_t)a.scenes * a.row_tiles;
+    const int32_t n = a.scenes * a.row_tiles;
     int64_t before = 0;
-    for (int64_t e0 = 0; e0 < n; e0 += 32) {
+    for (int32_t e0 = 0; e0 < n; e0 += 32) {
         int64_t c = e0 + lane < n ? entry_tiles(a, e0 + lane) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -138,15 +139,21 @@ struct Segment {
 // Walks the CTA's run; every role of the CTA makes the same walk.
 struct Walk {
     int64_t left;  // key tiles still to come
-    int64_t e;
-    int32_t h, t;
+    int32_t e, h, t;
+    // Starts at key tile x0 of the list: entry e0 and the tile's index within it.
+    __device__ __forceinline__ void start(const AttnArgs& a, int32_t e0, int64_t within) {
+        e = e0;
+        const int32_t tiles = (int32_t)(entry_tiles(a, e0) / a.kv_heads);
+        h = (int32_t)(within / tiles);
+        t = (int32_t)(within - (int64_t)h * tiles);
+    }
     __device__ __forceinline__ bool next(const AttnArgs& a, Segment* g) {
         if (left <= 0) return false;
-        const int64_t n = (int64_t)a.scenes * a.row_tiles;
+        const int32_t n = a.scenes * a.row_tiles;
         for (;;) {
             if (e >= n) return false;
-            g->s = (int32_t)(e / a.row_tiles);
-            g->rt = (int32_t)(e % a.row_tiles);
+            g->s = e / a.row_tiles;
+            g->rt = e - g->s * a.row_tiles;
             g->sc = scene_of(a, g->s);
             g->tiles = key_tiles(a, g->sc, g->rt);
             if (g->tiles > 0 && h < a.kv_heads) break;
@@ -235,17 +242,11 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     walk.left = min(cut.per, cut.total - x0);
     if (warp == 0 && walk.left > 0) {
         int64_t within;
-        const int64_t e = find_entry(a, x0, &within);
+        const int32_t e = find_entry(a, x0, &within);
         if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
     }
     __syncthreads();
-    if (walk.left > 0) {
-        walk.e = walk_smem[0];
-        const int64_t within = walk_smem[1];
-        const int32_t tiles = (int32_t)(entry_tiles(a, walk.e) / a.kv_heads);
-        walk.h = (int32_t)(within / tiles);
-        walk.t = (int32_t)(within % tiles);
-    }
+    if (walk.left > 0) walk.start(a, (int32_t)walk_smem[0], walk_smem[1]);
 
     const int page = 1 << a.page_log2, sub_pages = 128 >> a.page_log2;
     Segment g;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         bool ok = true, first_seg = true;
         while (ok && walk.next(a, &g)) {
             const int32_t nv = valid_rows(a, g.sc, g.rt);
-            const int64_t r0 = (int64_t)g.rt * a.tile_rows;
+            const int32_t r0 = g.rt * a.tile_rows;
             // Q^T operand: row 8 i + qg, channels 16 qc .. 16 qc + 15
             uint32_t qb[NT][8];
             int32_t lim[NT][2];  // key limits of this lane's columns, rows 8 i + 2 qc and the next
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int32_t x = 8 * i + 2 * qc + j;
-                    lim[i][j] = x < nv ? key_limit(a, g.sc, (int32_t)((r0 + x) / a.group)) : 0x7FFFFFFF;
+                    lim[i][j] = x < nv ? key_limit(a, g.sc, (r0 + x) / a.group) : 0x7FFFFFFF;
                     least = min(least, lim[i][j]);
                 }
             }
@@ -537,16 +538,15 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
     __shared__ int64_t before_smem;
     __shared__ float4 acc_smem[4][8][16];
     __shared__ float ml_smem[4][2][8];
-    const int64_t e = blockIdx.x / a.kv_heads;
-    const int h = (int)(blockIdx.x % a.kv_heads);
-    const int s = (int)(e / a.row_tiles), rt = (int)(e % a.row_tiles);
+    const int32_t e = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
+    const int32_t s = e / a.row_tiles, rt = e % a.row_tiles;
     const Scene sc = scene_of(a, s);
     const int32_t nv = valid_rows(a, sc, rt), tiles = key_tiles(a, sc, rt);
     const int grp = threadIdx.x / 128, x = (threadIdx.x / 16) % 8, c4 = threadIdx.x % 16;
     const int row_in = 8 * blockIdx.y + x;
     if (8 * (int)blockIdx.y >= nv || tiles == 0) {
         if (grp == 0 && row_in < nv) {  // rows that see no key
-            const int64_t row = out_row(a, s, h, (int64_t)rt * a.tile_rows + row_in);
+            const int64_t row = out_row(a, s, h, rt * a.tile_rows + row_in);
             *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) = make_uint2(0u, 0u);
             if (a.lse && c4 == 0) a.lse[row] = -INFINITY;
         }
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
     // key tiles before this problem
     int64_t sum = 0;
     __syncthreads();
-    for (int64_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_tiles(a, y);
+    for (int32_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_tiles(a, y);
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
         acc.w += v.w * w;
         l += ml_smem[y][1][x] * w;
     }
-    const int64_t row = out_row(a, s, h, (int64_t)rt * a.tile_rows + row_in);
+    const int64_t row = out_row(a, s, h, rt * a.tile_rows + row_in);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

@@ -3,15 +3,17 @@
 // scores in tensor memory.  The decoding of the pages and the exponentials share the SM with them, so
 // two thread blocks stay resident per SM and fill each other's waits.
 // Roles (384 threads):
-//   warps 0-3  softmax: thread r owns query row r.  One pass over a tile's 128 scores: the running
-//              maximum is the one of the tiles before, so the exponentials need not wait for the
-//              tile's own; only when a score is over it by more than 2^8 (a tile or two per problem)
-//              is the tile done again with the raised one.  P goes to tensor memory as bf16.
+//   warps 0-3  softmax: thread r owns query row r and takes a tile's scores in halves of 64.  The
+//              running maximum is raised (and O rescaled) only when a score is over it by more
+//              than 2^8, once or twice per problem.  P goes to tensor memory as bf16, a half at a
+//              time, each with barriers of its own: a half waits for no product but the one of the
+//              same half a tile before.
 //   warps 4-7  decode: a thread takes one key's K (4 blocks of 16 channels) and one 8 channel x 8 key
 //              patch of V straight from the pages into registers, a tile ahead, and writes bf16
 //              operands: K [128 keys][64], V^T [64][128 keys], both K-major with the 128-byte
 //              swizzle (eight lanes write the eight 16-byte chunks of a row: no bank conflicts).
-//   warp 8     (of a third warpgroup, whose registers go to the softmax) tensor-core issue: S = Q K^T of the next tile before O += P V of this one.
+//   warp 8     (of a third warpgroup, whose registers go to the other two) tensor-core issue: per tile
+//              the first half of P V, then S = Q K^T of the next tile, then the second half.
 // TMEM (256 columns a block): S 128 (f32), P 64 (bf16 pairs), O 64 (f32).
 #pragma once
 #include "k_kv_attn.cuh"
@@ -21,7 +23,7 @@ namespace kv {
 struct TcLayoutKv {
     static constexpr int kThreads = 384;
     // registers per thread after the split (launched with 80 each; the sum is the launch's own)
-    static constexpr uint32_t kRegsSoftmax = 104, kRegsDecode = 80, kRegsIssue = 56;
+    static constexpr uint32_t kRegsSoftmax = 112, kRegsDecode = 80, kRegsIssue = 48;
     static constexpr uint32_t kRegsNeeded = 128 * (kRegsSoftmax + kRegsDecode + kRegsIssue);
     static constexpr int kStages = 2;
     static constexpr int kTile = 128 * 128;  // bytes of a 128 x 64 bf16 operand
@@ -29,10 +31,11 @@ struct TcLayoutKv {
     static constexpr int kK = kQ + kTile;
     static constexpr int kV = kK + kStages * kTile;
     static constexpr int kBars = kV + kStages * kTile;
-    // k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_free, p_full, pv_done, drain
-    static constexpr int kNumBars = 4 * kStages + 6;
+    // k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_free, p_full[2], pv_done[2], drain
+    static constexpr int kNumBars = 4 * kStages + 8;
     static constexpr int kBad = kBars + 8 * kNumBars;  // [4 tiles][8 sub-pages] bytes
-    static constexpr int kMisc = kBad + 32;            // abort flag, tmem base, walk[2], reduction[12]
+    static constexpr int kSeg = kBad + 32;             // tiles of the problem whose Q has come
+    static constexpr int kMisc = kSeg + 8;             // abort flag, tmem base, walk[2], reduction[12]
     static constexpr int kEnd = kMisc + 8 + 16 + 96;
     static constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;
     static constexpr int smem_bytes() { return 1024 + kEnd; }
@@ -177,9 +180,10 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
     uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6;
-    uint64_t *q_full = bars + 8, *s_full = bars + 9, *s_free = bars + 10, *p_full = bars + 11, *pv_done = bars + 12,
-             *drain_bar = bars + 13;
+    uint64_t *q_full = bars + 8, *s_full = bars + 9, *s_free = bars + 10, *p_full = bars + 11, *pv_done = bars + 13,
+             *drain_bar = bars + 15;
     volatile uint8_t* bad_pages = smem + L::kBad;
+    volatile int* seg_tiles = reinterpret_cast<volatile int*>(smem + L::kSeg);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(smem + L::kMisc + 4);
     int64_t* walk_smem = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);
@@ -196,8 +200,10 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
         mbar_init(q_full, 4);
         mbar_init(s_full, 2);  // the products' completion, and the issuing thread's release of bad_pages
         mbar_init(s_free, 4);
-        mbar_init(p_full, 4);
-        mbar_init(pv_done, 1);
+        for (int i = 0; i < 2; ++i) {  // of a tile's two 64-key halves
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -212,7 +218,7 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
     }
     if (warp == 0) {
         int64_t within;
-        const int64_t e = find_entry(a, x0, &within);
+        const int32_t e = find_entry(a, x0, &within);
         if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
     }
     if (warp == 8) {
@@ -223,13 +229,7 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
-    {
-        walk.e = walk_smem[0];
-        const int64_t within = walk_smem[1];
-        const int32_t tiles = (int32_t)(entry_tiles(a, walk.e) / a.kv_heads);
-        walk.h = (int32_t)(within / tiles);
-        walk.t = (int32_t)(within % tiles);
-    }
+    walk.start(a, (int32_t)walk_smem[0], walk_smem[1]);
 
     if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------------ decode
@@ -273,52 +273,59 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
         const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + L::kK), 16, 1024);
         const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + L::kV), 16, 1024);
         constexpr uint64_t kStep = L::kTile >> 4;
-        Segment g;
         int it = 0, seg = 0;
         bool ok = true, any_mma = false;
-        while (ok && walk.next(a, &g)) {
-            const int n_tiles = g.t1 - g.t0;
-            ok = mbar_wait_warp(q_full, seg & 1, abort_flag);
+        for (;;) {
+            // the softmax warps say with each Q how many tiles follow, and with none that all is done
+            if (!mbar_wait_warp(q_full, seg & 1, abort_flag)) break;
+            const int n_tiles = *seg_tiles;
+            if (n_tiles == 0) break;
+            // S of tile n goes out between the two halves of P V of tile n - 1
             for (int n = 0; n <= n_tiles && ok; ++n) {
-                if (n < n_tiles) {
-                    const int i = it + n, st = i & 1;
-                    if (!mbar_wait_warp(&k_full[st], (i >> 1) & 1, abort_flag) ||
-                        (i > 0 && !mbar_wait_warp(s_free, (i - 1) & 1, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_ss(tmem + L::kColS, dq + 2 * kk, dk0 + st * kStep + 2 * kk, kIdescS, kk > 0);
-                        umma_commit(&k_empty[st]);
-                        umma_commit(s_full);
-                        mbar_arrive(s_full);
-                    }
-                    __syncwarp();
-                    any_mma = true;
-                }
-                if (n >= 1) {
-                    const int i = it + n - 1, st = i & 1;
-                    if (!mbar_wait_warp(&v_full[st], (i >> 1) & 1, abort_flag) ||
-                        !mbar_wait_warp(p_full, i & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (leader) {
+                for (int part = 0; part < 3; ++part) {
+                    if (part == 1) {
+                        if (n == n_tiles) continue;
+                        const int i = it + n, st = i & 1;
+                        if (!mbar_wait_warp(&k_full[st], (i >> 1) & 1, abort_flag) ||
+                            (i > 0 && !mbar_wait_warp(s_free, (i - 1) & 1, abort_flag))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_ts(tmem + L::kColO, tmem + L::kColP + 8 * kk,
-                                    dv0 + st * kStep + (uint64_t)((kk >> 2) * (8192 >> 4) + (kk & 3) * 2), kIdescPV,
-                                    n > 1 || kk > 0);
-                        umma_commit(&v_empty[st]);
-                        umma_commit(pv_done);
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_ss(tmem + L::kColS, dq + 2 * kk, dk0 + st * kStep + 2 * kk, kIdescS, kk > 0);
+                            umma_commit(&k_empty[st]);
+                            umma_commit(s_full);
+                            mbar_arrive(s_full);
+                        }
+                        __syncwarp();
+                        any_mma = true;
+                    } else {
+                        if (n == 0) continue;
+                        const int i = it + n - 1, st = i & 1, half = part / 2;
+                        if ((half == 0 && !mbar_wait_warp(&v_full[st], (i >> 1) & 1, abort_flag)) ||
+                            !mbar_wait_warp(&p_full[half], i & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_ts(tmem + L::kColO, tmem + L::kColP + 32 * half + 8 * kk,
+                                        dv0 + st * kStep + (uint64_t)(half * (8192 >> 4) + kk * 2), kIdescPV,
+                                        n > 1 || half > 0 || kk > 0);
+                            if (half == 1) umma_commit(&v_empty[st]);
+                            umma_commit(&pv_done[half]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
+            if (!ok) break;
             it += n_tiles;
             ++seg;
         }
@@ -341,7 +348,7 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
         bool ok = true, first_seg = true;
         while (ok && walk.next(a, &g)) {
             const int32_t nv = valid_rows(a, g.sc, g.rt);
-            const int64_t x = (int64_t)g.rt * a.tile_rows + r;
+            const int32_t x = g.rt * a.tile_rows + r;
             const int64_t row = out_row(a, g.s, g.h, x);
             // the products that read the last Q are done: their scores have been read
             {
@@ -354,14 +361,14 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
                 }
             }
             fence_proxy_async_smem();
+            if (r == 0) *seg_tiles = g.t1 - g.t0;
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            const int32_t lim = r < nv ? key_limit(a, g.sc, (int32_t)(x / a.group)) : g.sc.len;
+            const int32_t lim = r < nv ? key_limit(a, g.sc, x / a.group) : g.sc.len;
             const int32_t least = __reduce_min_sync(0xffffffffu, lim);
             float m_run = -INFINITY, l_run = 0.0f;
             for (int t = g.t0; t < g.t1; ++t, ++it) {
-                if (!mbar_wait_warp(s_full, it & 1, abort_flag) ||
-                    (t > g.t0 && !mbar_wait_warp(pv_done, (it - 1) & 1, abort_flag))) {
+                if (!mbar_wait_warp(s_full, it & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -372,82 +379,105 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
                 const bool bad = (bad8.x & (subs >= 4 ? ~0u : (1u << (8 * subs)) - 1u)) != 0 || (subs == 8 && bad8.y != 0);
                 const bool masked = (int64_t)t * 128 + 128 > least || bad;
                 const int32_t keys = min(max(lim - t * 128, 0), 128);
-                float2 acc;
-                for (;;) {
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t tSh = tS + 64 * half;
+                    uint32_t sv[64];
+                    uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv);
+                    uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32);
+                    tmem_ld_32x32b_x32(tSh, s0);
+                    tmem_ld_32x32b_x32(tSh + 32, s1);
+                    tmem_ld_wait(s0);
+                    reg_fence(s1);
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int col = 64 * half + 16 * c, k0 = min(max(keys - col, 0), 16);
+                            uint32_t seen = (1u << k0) - 1u;
+                            if (bad && bad_pages[(it & 3) * 8 + (col >> a.page_log2)]) seen = 0;
+#pragma unroll
+                            for (int u = 0; u < 16; ++u)
+                                if (!((seen >> u) & 1u)) sv[16 * c + u] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    float m8[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) m8[u] = __uint_as_float(sv[u]);
+#pragma unroll
+                    for (int c = 8; c < 56; c += 16)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            m8[u] = fmax3(m8[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 8 + u]));
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], __uint_as_float(sv[56 + u]));
+                    const float mx = mul * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                    if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
+                        // raise the maximum of the rows that need it and rescale what was summed, once every
+                        // product so far is done
+                        const float m_new = mx > m_run + 8.0f ? mx : m_run;
+                        const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
+                        m_run = m_new;
+                        l_run *= alpha;
+                        if (t > g.t0 || half > 0) {
+                            // the half before: of this tile, or the second one of the tile before
+                            if (!mbar_wait_warp(&pv_done[half ^ 1], (half ? it : it - 1) & 1, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < 64; c += 8) {
+                                uint32_t ov[8];
+                                tmem_ld_32x32b_x8(tO + c, ov);
+                                tmem_ld_wait8(ov);
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
+                                tmem_st_32x32b_x8(tO + c, ov);
+                            }
+                        }
+                    }
                     const float m_use = m_run == -INFINITY ? 0.0f : m_run;
                     const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-m_use, -m_use);
-                    float mx = -INFINITY;
-                    bool again = false;
-                    acc = make_float2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s[32];
-                        tmem_ld_32x32b_x32(tS + 32 * c, s);
-                        tmem_ld_wait(s);
-                        if (masked) {
-                            const int k0 = min(max(keys - 32 * c, 0), 32);
-                            uint32_t seen = k0 == 32 ? ~0u : (1u << k0) - 1u;
-                            if (bad)
-                                for (int u = 0; u < 32; u += 16)
-                                    if (bad_pages[(it & 3) * 8 + ((32 * c + u) >> a.page_log2)]) seen &= ~(0xFFFFu << u);
+                    float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-                            for (int u = 0; u < 32; ++u)
-                                if (!((seen >> u) & 1u)) s[u] = __float_as_uint(-INFINITY);
-                        }
-                        float m8[4] = {mx, mx, mx, mx};
-#pragma unroll
-                        for (int u = 0; u < 32; u += 8)
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                m8[w] = fmax3(m8[w], __uint_as_float(s[u + w]), __uint_as_float(s[u + 4 + w]));
-                        mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), m8[3]);
-                        if (c == 3) {
-                            again = __any_sync(0xffffffffu, mx * mul > m_run + 8.0f);
-                            if (again) break;
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(s_free);
-                        }
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int u = 0; u < 16; ++u) {
-                            const float2 xv = __ffma2_rn(
-                                make_float2(__uint_as_float(s[2 * u]), __uint_as_float(s[2 * u + 1])), mul2, neg2);
+                            const float2 xv = __ffma2_rn(make_float2(__uint_as_float(sv[32 * c + 2 * u]),
+                                                                     __uint_as_float(sv[32 * c + 2 * u + 1])),
+                                                         mul2, neg2);
                             float2 p;
                             p.x = ex2_approx(xv.x);
                             p.y = ex2_approx(xv.y);
                             acc = __fadd2_rn(acc, p);
                             pk[u] = pack_bf16x2(p.x, p.y);
                         }
-                        tmem_st_32x32b_x16(tP + 16 * c, pk);
-                    }
-                    if (!again) break;
-                    // raise the maximum of the rows that need it, rescale what was summed, do the tile again
-                    const float mxs = mx * mul;
-                    const float m_new = mxs > m_run + 8.0f ? mxs : m_run;
-                    const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
-                    m_run = m_new;
-                    l_run *= alpha;
-                    tmem_st_wait();
-                    if (t > g.t0) {
-#pragma unroll
-                        for (int c = 0; c < 64; c += 16) {
-                            uint32_t ov[16];
-                            tmem_ld_32x32b_x16(tO + c, ov);
-                            tmem_ld_wait16(ov);
-#pragma unroll
-                            for (int u = 0; u < 16; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
-                            tmem_st_32x32b_x16(tO + c, ov);
+                        // this half's place for P is free once its product of the tile before is done
+                        if (c == 0 && t > g.t0) {
+                            if (!mbar_wait_warp(&pv_done[half], (it - 1) & 1, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
                         }
+                        tmem_st_32x32b_x16(tP + 32 * half + 16 * c, pk);
                     }
+                    if (!ok) break;
+                    l_run += acc.x + acc.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[half]);
                 }
-                l_run += acc.x + acc.y;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full);
+                if (!ok) break;
             }
-            if (!ok || !mbar_wait_warp(pv_done, (it - 1) & 1, abort_flag)) {
+            if (!ok || !mbar_wait_warp(&pv_done[1], (it - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -490,6 +520,11 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
                 }
             }
             first_seg = false;
+        }
+        if (ok) {
+            if (r == 0) *seg_tiles = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
         }
     }
 

@@ -1375,7 +1375,7 @@ sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvG
     const sa_status st = kv_geo(c, g);
     if (st != SA_OK) return st;
     if (q_heads < 1 || q_heads % c->heads != 0 || rows < 1) return SA_ERR_INVALID_ARG;
-    if ((int64_t)c->scenes * q_heads >= (int64_t(1) << 31) || (int64_t)c->scenes * q_heads * rows >= (int64_t(1) << 31))
+    if ((int64_t)c->scenes * q_heads >= (int64_t(1) << 31) || (int64_t)c->scenes * q_heads * rows > (int64_t(1) << 31) - 256)
         return SA_ERR_UNSUPPORTED;
     return SA_OK;
 }
