@@ -3,10 +3,10 @@
 //
 // Work is a list of (scene, tile of query rows, head) problems, each a run of 128-key tiles; their
 // number is known on the device only (lengths are device memory, so that a captured call follows
-// them).  The concatenated list of key tiles is cut into equal runs, one per CTA, whatever the
-// lengths; a CTA that holds all tiles of a problem writes its rows, otherwise it leaves (O, max,
-// sum) of its part in the workspace and kv_merge_kernel joins the parts in a fixed order (no
-// atomics: results do not depend on timing).
+// them).  The concatenated list of key tiles, each with its cost, is cut into runs of equal cost,
+// one per CTA, whatever the lengths; a CTA that holds all tiles of a problem writes its rows,
+// otherwise it leaves (O, max, sum) of its part in the workspace and kv_merge_kernel joins the
+// parts in a fixed order (no atomics: results do not depend on timing).
 #pragma once
 #include "k_attn_tc.cuh"
 #include "k_kv_cache.cuh"
@@ -26,8 +26,8 @@ struct AttnArgs {
     int32_t scenes, kv_heads, group, rows;
     int32_t tile_rows, row_tiles;  // query rows per problem, problems per (scene, head)
     int32_t page_log2, n_pages, max_pages, frame;
-    int32_t ctas, min_tiles;  // grid of the attention kernel, least tiles of a CTA
-    int64_t page_bytes;
+    int32_t ctas, min_units;  // grid of the attention kernel, least cost of a CTA's run
+    int64_t page_bytes, page_stride;  // of one page of one head, of a page of every head
     float scale_log2;
 };
 
@@ -74,44 +74,64 @@ __device__ __forceinline__ bool all_agree(uint32_t id, uint32_t nthreads, bool m
         : "memory");
     return r != 0;
 }
+// A bounded wait whose first tries take no clock: reading the timer and the limit costs more than most
+// of these waits last.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    bool ok = false;
+#pragma unroll 1
+    for (int i = 0; i < 200 && !ok; ++i) ok = mbar_test(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, abort_flag);
+    return __all_sync(0xffffffffu, ok);
+}
 // Waits until the kernel before this one in the stream, whose end this one was launched ahead of, is
 // done and its writes are seen.  Every thread of such a kernel comes through here before it ends, so
 // that what follows in the stream follows both.
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The tensor-core kernel takes 256 rows a problem, 128 in each half of a block.  One that has at most
+// 128 of them is done by both halves together, every other key tile each ("solo").  Cost of a key tile:
+// about its time (a solo tile has half the work, but the whole decoding).
+constexpr int kPairRows = 256;
+constexpr int kPairCost = 4, kSoloCost = 3;
+__device__ __forceinline__ bool is_solo(const AttnArgs& a, int32_t nv) { return a.tile_rows == kPairRows && nv <= 128; }
+__device__ __forceinline__ int32_t tile_cost(const AttnArgs& a, int32_t nv) {
+    return a.tile_rows != kPairRows ? 1 : nv > 128 ? kPairCost : kSoloCost;
+}
+
 // The list of problems, entry e = (scene e / row_tiles, row tile e % row_tiles), heads within.
 struct Cut {
-    int64_t total;  // key tiles of all problems
-    int64_t per;    // of one CTA
+    int64_t total;  // cost of all key tiles
+    int64_t per;    // of one CTA's run
 };
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-__device__ __forceinline__ int64_t entry_tiles(const AttnArgs& a, int32_t e) {
-    const int s = e / a.row_tiles;
-    return (int64_t)key_tiles(a, scene_of(a, s), e - s * a.row_tiles) * a.kv_heads;
+__device__ __forceinline__ int64_t entry_cost(const AttnArgs& a, int32_t e) {
+    const int s = e / a.row_tiles, rt = e - s * a.row_tiles;
+    const Scene sc = scene_of(a, s);
+    return (int64_t)key_tiles(a, sc, rt) * tile_cost(a, valid_rows(a, sc, rt)) * a.kv_heads;
 }
-// Every warp of the block calls it; `red` is shared memory of one int64 per warp.
+// Every thread of the block calls it; `red` is shared memory of one int64 per warp.
 __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int64_t* red) {
     const int32_t n = a.scenes * a.row_tiles;
     int64_t sum = 0;
-    for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_tiles(a, e);
+    for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e);
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
     __syncthreads();
     sum = 0;
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += red[w];
-    return Cut{sum, max((sum + a.ctas - 1) / a.ctas, (int64_t)a.min_tiles)};
+    return Cut{sum, max((sum + a.ctas - 1) / a.ctas, (int64_t)a.min_units)};
 }
-// The entry that holds key tile x of the list (x < total), and the tile's index within it.  One warp.
+// The entry that holds place x of the list (x < total), and the place within it.  One warp.
 __device__ __forceinline__ int32_t find_entry(const AttnArgs& a, int64_t x, int64_t* within) {
     const int lane = threadIdx.x & 31;
     const int32_t n = a.scenes * a.row_tiles;
     int64_t before = 0;
     for (int32_t e0 = 0; e0 < n; e0 += 32) {
-        int64_t c = e0 + lane < n ? entry_tiles(a, e0 + lane) : 0;
+        int64_t c = e0 + lane < n ? entry_cost(a, e0 + lane) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
@@ -134,44 +154,51 @@ __device__ __forceinline__ int32_t find_entry(const AttnArgs& a, int64_t x, int6
 struct Segment {
     int32_t s, rt, h;
     int32_t t0, t1, tiles;  // key tiles [t0, t1) of the problem's `tiles`
+    int32_t nv;             // its rows
     Scene sc;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+    // Workspace slot of a part: a CTA leaves at most two, one of a problem that began before its run
+    // and one of a problem that goes on after it.
+    __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1); }
 };
-// Walks the CTA's run; every role of the CTA makes the same walk.
+// Walks the CTA's run; every role of the CTA makes the same walk.  A tile belongs to the run in which
+// its place in the list (cost by cost) begins.
 struct Walk {
-    int64_t left;  // key tiles still to come
-    int32_t e, h, t;
-    // Starts at key tile x0 of the list: entry e0 and the tile's index within it.
+    int64_t left, u;  // cost still to come, place within the problem at hand
+    int32_t e, h;
     __device__ __forceinline__ void start(const AttnArgs& a, int32_t e0, int64_t within) {
         e = e0;
-        const int32_t tiles = (int32_t)(entry_tiles(a, e0) / a.kv_heads);
-        h = (int32_t)(within / tiles);
-        t = (int32_t)(within - (int64_t)h * tiles);
+        const int64_t one = entry_cost(a, e0) / a.kv_heads;
+        h = (int32_t)(within / one);
+        u = within - h * one;
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, Segment* g) {
-        if (left <= 0) return false;
         const int32_t n = a.scenes * a.row_tiles;
-        for (;;) {
-            if (e >= n) return false;
+        while (left > 0 && e < n) {
             g->s = e / a.row_tiles;
             g->rt = e - g->s * a.row_tiles;
             g->sc = scene_of(a, g->s);
+            g->nv = valid_rows(a, g->sc, g->rt);
             g->tiles = key_tiles(a, g->sc, g->rt);
-            if (g->tiles > 0 && h < a.kv_heads) break;
-            ++e;
-            h = t = 0;
+            if (g->tiles == 0 || h >= a.kv_heads) {
+                ++e;
+                h = 0;
+                u = 0;
+                continue;
+            }
+            const int32_t cost = tile_cost(a, g->nv);
+            const int64_t u1 = min((int64_t)g->tiles * cost, u + left);
+            g->h = h;
+            g->t0 = (int32_t)((u + cost - 1) / cost);
+            g->t1 = (int32_t)((u1 + cost - 1) / cost);
+            left -= u1 - u;
+            u = 0;
+            ++h;
+            if (g->t0 < g->t1) return true;
         }
-        g->h = h;
-        g->t0 = t;
-        g->t1 = (int32_t)min((int64_t)g->tiles, t + left);
-        left -= g->t1 - g->t0;
-        t = 0;
-        ++h;
-        return true;
+        return false;
     }
 };
-// Workspace slot of a segment that is part of a problem: a CTA leaves at most two, the first and the
-// last of its run.
-__device__ __forceinline__ int part_slot(bool first) { return 2 * (int)blockIdx.x + (first ? 0 : 1); }
 
 // ------------------------------------------------------------------------------ few rows
 //
@@ -265,7 +292,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                 const bool good = mine && pid >= 0 && pid < a.n_pages;
                 const uint32_t bad = __ballot_sync(0xffffffffu, mine && !good);
                 const int n = __popc(__ballot_sync(0xffffffffu, good));
-                if (!mbar_wait_warp(&empty[st], ((it / L::kStages) & 1) ^ 1, abort_flag)) {
+                if (!wait_warp(&empty[st], ((it / L::kStages) & 1) ^ 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -286,9 +313,9 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     } else {
         // ---------------------------------------------------------------- products
         const int qg = lane >> 2, qc = lane & 3;
-        bool ok = true, first_seg = true;
+        bool ok = true;
         while (ok && walk.next(a, &g)) {
-            const int32_t nv = valid_rows(a, g.sc, g.rt);
+            const int32_t nv = g.nv;
             const int32_t r0 = g.rt * a.tile_rows;
             // Q^T operand: row 8 i + qg, channels 16 qc .. 16 qc + 15
             uint32_t qb[NT][8];
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
             }
             for (int t = g.t0; t < g.t1; ++t, ++it) {
                 const int st = it % L::kStages;
-                if (!mbar_wait_warp(&full[st], (it / L::kStages) & 1, abort_flag)) {
+                if (!wait_warp(&full[st], (it / L::kStages) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -480,10 +507,10 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                     }
                 }
             ok = all_agree(1, 32 * L::kWarps, ok);  // a wait that ran out ends all four warps here
-            const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+            const bool whole = g.whole();
             const float* all_ml = reinterpret_cast<const float*>(smem + L::kMergeMl);
             const float* all_o = reinterpret_cast<const float*>(smem + L::kMergeO);
-            const int slot = part_slot(first_seg);
+            const int slot = g.slot();
             if (ok)
                 for (int x = threadIdx.x / 16; x < nv; x += 8) {
                     const int c4 = threadIdx.x % 16;
@@ -519,7 +546,6 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                         }
                     }
                 }
-            first_seg = false;
             named_bar_sync(1, 32 * L::kWarps);
         }
     }
@@ -528,9 +554,9 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 
 // ------------------------------------------------------------------------------ joining the parts
 //
-// One block per (entry, head, 8 rows): rows of a problem that several CTAs shared, and rows of one
-// that has no keys at all.  Four groups of threads sum every fourth part, in order, then the groups
-// in order.
+// One block per (entry, head, 8 rows): rows of a problem that several CTAs shared, and rows of one that
+// has no keys at all.  Four groups of threads sum every fourth part, in
+// order, then the groups in order.
 constexpr int kMergeThreads = 512;
 
 __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs a) {
@@ -554,32 +580,32 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
         return;
     }
     const Cut cut = cut_of(a, red);
-    // key tiles before this problem
+    // place of this problem's first tile in the list
     int64_t sum = 0;
     __syncthreads();
-    for (int32_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_tiles(a, y);
+    for (int32_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_cost(a, y);
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
     __syncthreads();
+    const int32_t cost = tile_cost(a, nv);
     if (threadIdx.x == 0) {
         int64_t b = 0;
         for (int w = 0; w < kMergeThreads / 32; ++w) b += red[w];
-        before_smem = b + (int64_t)h * tiles;
+        before_smem = b + (int64_t)h * tiles * cost;
     }
     __syncthreads();
-    const int64_t g0 = before_smem, g1 = g0 + tiles;
-    const int c0 = (int)(g0 / cut.per), c1 = (int)((g1 - 1) / cut.per);
+    const int64_t g0 = before_smem;
+    const int c0 = (int)(g0 / cut.per), c1 = (int)((g0 + (int64_t)(tiles - 1) * cost) / cut.per);
     wait_previous_kernel();
     if (c0 == c1) return;  // one CTA had all of it and wrote the rows
     float m = -INFINITY, l = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row_in < nv) {
         for (int c = c0 + grp; c <= c1; c += 4) {
-            const int64_t slot = 2 * (int64_t)c + (g0 <= c * cut.per ? 0 : 1);
+            const int64_t slot = 2 * (int64_t)c + (c == c0 ? 1 : 0);
             const float pm = __ldcg(a.part_ml + slot * 2 * a.tile_rows + row_in);
             const float pl = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + row_in);
-            const float4 v =
-                __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + row_in) * 64 + 4 * c4));
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + row_in) * 64 + 4 * c4));
             const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.0f : mn;
             const float f = ex2_approx(m - mu), w = ex2_approx(pm - mu);
             acc.x = acc.x * f + v.x * w;

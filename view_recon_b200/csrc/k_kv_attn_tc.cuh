@@ -1,76 +1,71 @@
 // Attention over the frame cache for more than 32 query rows a problem (whole frames): the
-// products on the 5th-generation tensor cores, 128 query rows against 128 keys at a time, O and the
-// scores in tensor memory.  The decoding of the pages and the exponentials share the SM with them, so
-// two thread blocks stay resident per SM and fill each other's waits.
-// Roles (384 threads):
-//   warps 0-3  softmax: thread r owns query row r and takes a tile's scores in halves of 64.  The
-//              running maximum is raised (and O rescaled) only when a score is over it by more
-//              than 2^8, once or twice per problem.  P goes to tensor memory as bf16, a half at a
-//              time, each with barriers of its own: a half waits for no product but the one of the
-//              same half a tile before.
-//   warps 4-7  decode: a thread takes one key's K (4 blocks of 16 channels) and one 8 channel x 8 key
-//              patch of V straight from the pages into registers, a tile ahead, and writes bf16
-//              operands: K [128 keys][64], V^T [64][128 keys], both K-major with the 128-byte
-//              swizzle (eight lanes write the eight 16-byte chunks of a row: no bank conflicts).
-//   warp 8     (of a third warpgroup, whose registers go to the other two) tensor-core issue: per tile
-//              the first half of P V, then S = Q K^T of the next tile, then the second half.
-// TMEM (256 columns a block): S 128 (f32), P 64 (bf16 pairs), O 64 (f32).
+// products on the 5th-generation tensor cores, 128 keys a step, scores and O in tensor memory.
+// One block per SM, two halves: each takes 128 of a problem's 256 query rows through the same decoded
+// keys, so that a page is decoded once for both and one half's exponentials fill the other's waits.  A
+// problem of at most 128 rows is done "solo": both halves hold the same rows, take every other tile
+// and join their results through shared memory.
+// Roles (512 threads):
+//   warps 0, 1   tensor-core issue of half 0, 1: S = Q K^T of the next tile before O += P V of this one
+//   warps 4-7    decode: a thread takes one key's K (4 blocks of 16 channels) and one 8 channel x 8 key
+//                patch of V straight from the pages into registers, a tile ahead, and writes bf16
+//                operands: K [128 keys][64], V^T [64][128 keys], both K-major with the 128-byte
+//                swizzle (eight lanes write the eight 16-byte chunks of a row: no bank conflicts)
+//   warps 8-15   softmax of half 0, 1: thread r owns row r.  The running maximum is raised (and O
+//                rescaled) only when a score is over it by more than 2^8; P goes to tensor memory as bf16
+// TMEM (512 columns), per half: S 128 (f32), P 64 (bf16 pairs), O 64 (f32).
 #pragma once
 #include "k_kv_attn.cuh"
 
 namespace kv {
 
 struct TcLayoutKv {
-    static constexpr int kThreads = 384;
-    // registers per thread after the split (launched with 80 each; the sum is the launch's own)
-    static constexpr uint32_t kRegsSoftmax = 112, kRegsDecode = 80, kRegsIssue = 48;
-    static constexpr uint32_t kRegsNeeded = 128 * (kRegsSoftmax + kRegsDecode + kRegsIssue);
-    static constexpr int kStages = 2;
+    static constexpr int kThreads = 512;
+    // registers per thread after the split (launched with 128 each; the sum is the launch's own)
+    static constexpr uint32_t kRegsIssue = 48, kRegsDecode = 96, kRegsSoftmax = 184;
+    static constexpr uint32_t kRegsNeeded = 128 * (kRegsIssue + kRegsDecode + 2 * kRegsSoftmax);
+    static constexpr int kStages = 4;
     static constexpr int kTile = 128 * 128;  // bytes of a 128 x 64 bf16 operand
-    static constexpr int kQ = 0;
-    static constexpr int kK = kQ + kTile;
-    static constexpr int kV = kK + kStages * kTile;
-    static constexpr int kBars = kV + kStages * kTile;
-    // k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, s_full, s_free, p_full[2], pv_done[2], drain
-    static constexpr int kNumBars = 4 * kStages + 8;
-    static constexpr int kBad = kBars + 8 * kNumBars;  // [4 tiles][8 sub-pages] bytes
-    static constexpr int kSeg = kBad + 32;             // tiles of the problem whose Q has come
-    static constexpr int kMisc = kSeg + 8;             // abort flag, tmem base, walk[2], reduction[12]
-    static constexpr int kEnd = kMisc + 8 + 16 + 96;
-    static constexpr uint32_t kTmemCols = 256, kColS = 0, kColP = 128, kColO = 192;
+    static constexpr int kQ = 0;                            // [half]
+    static constexpr int kKV = kQ + 2 * kTile;              // [stage] K, V^T
+    static constexpr int kBars = kKV + 2 * kStages * kTile;
+    // kv_full[stage], kv_empty[stage]; per half: q_full, s_full, s_free, p_full, pv_done, drain, q_seen; solo: x_full, x_empty
+    static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2;
+    static constexpr int kBad = kBars + 8 * kNumBars;      // [stage][8 sub-pages] bytes
+    static constexpr int kSeg = kBad + 8 * kStages;        // per half: tiles of the problem at hand, solo flag
+    static constexpr int kMisc = kSeg + 16;                // abort flag, tmem base, walk[2], reduction[16]
+    static constexpr int kJoin = kMisc + 8 + 16 + 128;     // solo: half 1's O [64][128 rows], max, sum (f32)
+    static constexpr int kEnd = kJoin + 66 * 128 * 4;
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t colS(int x) { return 256 * x; }
+    static constexpr uint32_t colP(int x) { return 256 * x + 128; }
+    static constexpr uint32_t colO(int x) { return 256 * x + 192; }
     static constexpr int smem_bytes() { return 1024 + kEnd; }
     static_assert(kBars % 8 == 0 && kMisc % 8 == 0, "alignment");
 };
 
-// The tiles of a CTA's run one after the other, across its problems.
-struct TileCursor {
-    Walk walk;
-    Segment g;
-    int32_t t;
-    bool live;
-    __device__ __forceinline__ TileCursor(const AttnArgs& a, const Walk& w) : walk(w) {
-        live = walk.next(a, &g);
-        t = live ? g.t0 : 0;
+// Where the pages of a problem are: its row of the page table, its head's page 0, and the tokens that
+// any of its rows sees.
+struct PageRun {
+    const int32_t* row;
+    const uint8_t* head;
+    int32_t lim;
+    __device__ __forceinline__ PageRun(const AttnArgs& a, const Segment& g) {
+        row = a.table + (int64_t)g.s * a.max_pages;
+        head = a.pool + g.h * a.page_bytes;
+        lim = (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a) {
-        if (++t < g.t1) return;
-        live = walk.next(a, &g);
-        t = live ? g.t0 : 0;
+    // The page of token `key`, or null: past the limit, or a bad page.
+    __device__ __forceinline__ const uint8_t* of(const AttnArgs& a, int32_t key, bool* bad) const {
+        *bad = false;
+        if (key >= lim) return nullptr;
+        const uint32_t pid = (uint32_t)__ldg(row + (key >> a.page_log2));
+        if (pid >= (uint32_t)a.n_pages) {
+            *bad = true;
+            return nullptr;
+        }
+        return head + (int64_t)pid * a.page_stride;
     }
 };
-
-// Page base (of head h) that holds token `key` of the segment's scene, or null: past the keys that
-// any row sees, or a bad page.
-__device__ __forceinline__ const uint8_t* page_of(const AttnArgs& a, const Segment& g, int32_t key, bool* bad) {
-    *bad = false;
-    if (key >= (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len)) return nullptr;
-    const int32_t pid = __ldg(a.table + (int64_t)g.s * a.max_pages + (key >> a.page_log2));
-    if (pid < 0 || pid >= a.n_pages) {
-        *bad = true;
-        return nullptr;
-    }
-    return a.pool + ((int64_t)pid * a.kv_heads + g.h) * a.page_bytes;
-}
 
 __device__ __forceinline__ uint2 ld_shared_v2(const void* p) {
     uint2 v;
@@ -81,11 +76,9 @@ __device__ __forceinline__ uint2 ld_shared_v2(const void* p) {
 template <int BITS>
 struct KeyRegs {  // one key's K
     uint32_t w[4][Fmt<BITS>::kWords], scales;
-    bool bad;
-    __device__ __forceinline__ void load(const AttnArgs& a, const Segment& g, int32_t t, int tid) {
+    __device__ __forceinline__ void load(const AttnArgs& a, const uint8_t* base, int tid) {
         using F = Fmt<BITS>;
         const int page = 1 << a.page_log2, slot = tid & (page - 1);
-        const uint8_t* base = page_of(a, g, t * 128 + tid, &bad);
         if (!base) {
             scales = 0;
 #pragma unroll
@@ -123,11 +116,9 @@ struct ValueRegs {  // channels 8 ch8 .. + 7 of keys 8 oct .. + 7
     // lane l of decode warp y: octet (l & 7) + 8 (y & 1), channels 8 ((l >> 3) + 4 (y >> 1))
     static __device__ __forceinline__ int oct(int tid) { return (tid & 7) + ((tid >> 5) & 1) * 8; }
     static __device__ __forceinline__ int ch8(int tid) { return ((tid >> 3) & 3) + (tid >> 6) * 4; }
-    __device__ __forceinline__ void load(const AttnArgs& a, const Segment& g, int32_t t, int tid) {
+    __device__ __forceinline__ void load(const AttnArgs& a, const uint8_t* base, int tid) {
         using F = Fmt<BITS>;
         const int page = 1 << a.page_log2, slot = (8 * oct(tid)) & (page - 1);
-        bool bad;
-        const uint8_t* base = page_of(a, g, t * 128 + 8 * oct(tid), &bad);
         if (!base) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -174,37 +165,42 @@ struct ValueRegs {  // channels 8 ch8 .. + 7 of keys 8 oct .. + 7
 };
 
 template <int BITS>
-__global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     using L = TcLayoutKv;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
-    uint64_t *k_full = bars, *k_empty = bars + 2, *v_full = bars + 4, *v_empty = bars + 6;
-    uint64_t *q_full = bars + 8, *s_full = bars + 9, *s_free = bars + 10, *p_full = bars + 11, *pv_done = bars + 13,
-             *drain_bar = bars + 15;
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* kv_empty = kv_full + L::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = warp >= 8 ? (warp - 8) >> 2 : warp & 1;
+    uint64_t* bars = kv_empty + L::kStages + 7 * half;
+    uint64_t *q_full = bars, *s_full = bars + 1, *s_free = bars + 2, *p_full = bars + 3, *pv_done = bars + 4,
+             *drain_bar = bars + 5, *q_seen = bars + 6;
+    uint64_t *x_full = kv_empty + L::kStages + 14, *x_empty = x_full + 1;
     volatile uint8_t* bad_pages = smem + L::kBad;
-    volatile int* seg_tiles = reinterpret_cast<volatile int*>(smem + L::kSeg);
+    volatile int* seg = reinterpret_cast<volatile int*>(smem + L::kSeg) + 2 * half;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(smem + L::kMisc + 4);
     int64_t* walk_smem = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);
     int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 24);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kStages; ++i) {
-            mbar_init(&k_full[i], 4);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 4);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&kv_full[i], 4);
+            mbar_init(&kv_empty[i], 2);
         }
-        mbar_init(q_full, 4);
-        mbar_init(s_full, 2);  // the products' completion, and the issuing thread's release of bad_pages
-        mbar_init(s_free, 4);
-        for (int i = 0; i < 2; ++i) {  // of a tile's two 64-key halves
-            mbar_init(&p_full[i], 4);
-            mbar_init(&pv_done[i], 1);
+        for (int y = 0; y < 2; ++y) {
+            uint64_t* b = kv_empty + L::kStages + 7 * y;
+            mbar_init(&b[0], 4);  // q_full
+            mbar_init(&b[1], 2);  // s_full: the products' completion, and the issuing thread's release of bad_pages
+            mbar_init(&b[2], 4);  // s_free
+            mbar_init(&b[3], 4);  // p_full
+            mbar_init(&b[4], 1);  // pv_done
+            mbar_init(&b[5], 1);  // drain
+            mbar_init(&b[6], 1);  // q_seen
         }
-        mbar_init(drain_bar, 1);
+        mbar_init(x_full, 4);
+        mbar_init(x_empty, 4);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -220,8 +216,6 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
         int64_t within;
         const int32_t e = find_entry(a, x0, &within);
         if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
-    }
-    if (warp == 8) {
         tmem_alloc(tmem_base_smem, L::kTmemCols);
         tmem_relinquish();
     }
@@ -236,59 +230,89 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
         setmaxnreg_dec<L::kRegsDecode>();
         const int tid = threadIdx.x - 128;
         const bool withhold = g_sa_test_withhold != 0 && blockIdx.x == 0;
-        TileCursor c(a, walk);
-        KeyRegs<BITS> kr;
-        ValueRegs<BITS> vr;
-        if (c.live) {
-            kr.load(a, c.g, c.t, tid);
-            vr.load(a, c.g, c.t, tid);
-        }
-        for (int it = 0; c.live; ++it) {
-            const int st = it & 1, ph = (it >> 1) & 1;
-            if (!mbar_wait_warp(&k_empty[st], ph ^ 1, abort_flag)) break;
-            kr.store(smem + L::kK + st * L::kTile, tid);
-            if ((tid & ((1 << a.page_log2) - 1)) == 0) {
-                bad_pages[(it & 3) * 8 + (tid >> a.page_log2)] = kr.bad;
-                if (kr.bad) sa_flag_error(SA_ERR_BAD_LIST);
+        // The registers hold the tile that is written next; its page pointers were looked up a tile
+        // before it was loaded, and it was loaded a tile before it is written.
+        Segment g;
+        bool more = walk.next(a, &g);  // tile t of the problem at hand, up to t1
+        if (more) {
+            PageRun run(a, g);
+            int32_t t = g.t0, t1 = g.t1;
+            KeyRegs<BITS> kr;
+            ValueRegs<BITS> vr;
+            bool bad_now, bad_next, unused;
+            const uint8_t* pk = run.of(a, t * 128 + tid, &bad_now);
+            const uint8_t* pv = run.of(a, t * 128 + 8 * ValueRegs<BITS>::oct(tid), &unused);
+            kr.load(a, pk, tid);
+            vr.load(a, pv, tid);
+            auto advance = [&]() {
+                if (++t == t1 && (more = walk.next(a, &g))) {
+                    run = PageRun(a, g);
+                    t = g.t0;
+                    t1 = g.t1;
+                }
+                if (more) {
+                    pk = run.of(a, t * 128 + tid, &bad_next);
+                    pv = run.of(a, t * 128 + 8 * ValueRegs<BITS>::oct(tid), &unused);
+                }
+            };
+            advance();
+            for (int it = 0;; ++it) {
+                const int st = it % L::kStages;
+                if (!wait_warp(&kv_empty[st], ((it / L::kStages) & 1) ^ 1, abort_flag)) break;
+                uint8_t* tile = smem + L::kKV + st * 2 * L::kTile;
+                const bool last = !more;
+                kr.store(tile, tid);
+                if (!last) kr.load(a, pk, tid);
+                vr.store(tile + L::kTile, tid);
+                if ((tid & ((1 << a.page_log2) - 1)) == 0) {
+                    bad_pages[st * 8 + (tid >> a.page_log2)] = bad_now;
+                    if (bad_now) sa_flag_error(SA_ERR_BAD_LIST);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && !(withhold && it == 0)) mbar_arrive(&kv_full[st]);
+                if (last) break;
+                vr.load(a, pv, tid);
+                bad_now = bad_next;
+                advance();
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && !(withhold && it == 0)) mbar_arrive(&k_full[st]);
-            c.next(a);
-            if (c.live) kr.load(a, c.g, c.t, tid);
-            if (!mbar_wait_warp(&v_empty[st], ph ^ 1, abort_flag)) break;
-            vr.store(smem + L::kV + st * L::kTile, tid);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_full[st]);
-            if (c.live) vr.load(a, c.g, c.t, tid);
         }
-    } else if (warp >= 8) {
+    } else if (warp < 4) {
         // ------------------------------------------------------------------ tensor-core issue
         setmaxnreg_dec<L::kRegsIssue>();
-        if (warp == 8) {
-        constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, 64, 0);
-        const bool leader = tc::elect_one();
-        const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kQ), 16, 1024);
-        const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + L::kK), 16, 1024);
-        const uint64_t dv0 = smem_desc_sw128(smem_u32(smem + L::kV), 16, 1024);
-        constexpr uint64_t kStep = L::kTile >> 4;
-        int it = 0, seg = 0;
-        bool ok = true, any_mma = false;
-        for (;;) {
-            // the softmax warps say with each Q how many tiles follow, and with none that all is done
-            if (!mbar_wait_warp(q_full, seg & 1, abort_flag)) break;
-            const int n_tiles = *seg_tiles;
-            if (n_tiles == 0) break;
-            // S of tile n goes out between the two halves of P V of tile n - 1
-            for (int n = 0; n <= n_tiles && ok; ++n) {
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    if (part == 1) {
-                        if (n == n_tiles) continue;
-                        const int i = it + n, st = i & 1;
-                        if (!mbar_wait_warp(&k_full[st], (i >> 1) & 1, abort_flag) ||
-                            (i > 0 && !mbar_wait_warp(s_free, (i - 1) & 1, abort_flag))) {
+        if (warp < 2) {
+            constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, 64, 0);
+            const bool leader = tc::elect_one();
+            const uint64_t dq = smem_desc_sw128(smem_u32(smem + L::kQ + half * L::kTile), 16, 1024);
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(smem + L::kKV), 16, 1024);
+            constexpr uint64_t kStep = (2 * L::kTile) >> 4;
+            const uint32_t tS = tmem + L::colS(half), tP = tmem + L::colP(half), tO = tmem + L::colO(half);
+            int it = 0, own = 0, problem = 0;  // tiles, this half's tiles, problems so far
+            bool ok = true, any_mma = false;
+            for (;;) {
+                // the softmax warps say with each Q how many tiles follow, and with none that all is done
+                if (!wait_warp(q_full, problem & 1, abort_flag)) break;
+                const int n_tiles = seg[0], solo = seg[1];
+                if (n_tiles == 0) break;
+                __syncwarp();
+                if (leader) mbar_arrive(q_seen);
+                ++problem;
+                int last = -1;  // stage of this half's last tile, whose P V is still to come
+                const int first_own = own;
+                for (int n = 0; n <= n_tiles; ++n) {
+                    const bool mine = n < n_tiles && (!solo || (n & 1) == half);
+                    const int st = (it + n) % L::kStages;
+                    if (n < n_tiles && !wait_warp(&kv_full[st], ((it + n) / L::kStages) & 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (n < n_tiles && !mine) {  // the other half's tile
+                        if (leader) mbar_arrive(&kv_empty[st]);
+                        __syncwarp();
+                        continue;
+                    }
+                    if (mine) {
+                        if (own > 0 && !wait_warp(s_free, (own - 1) & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
@@ -296,233 +320,281 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
                         if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ss(tmem + L::kColS, dq + 2 * kk, dk0 + st * kStep + 2 * kk, kIdescS, kk > 0);
-                            umma_commit(&k_empty[st]);
+                                umma_ss(tS, dq + 2 * kk, dk0 + st * kStep + 2 * kk, kIdescS, kk > 0);
                             umma_commit(s_full);
                             mbar_arrive(s_full);
                         }
                         __syncwarp();
                         any_mma = true;
-                    } else {
-                        if (n == 0) continue;
-                        const int i = it + n - 1, st = i & 1, half = part / 2;
-                        if ((half == 0 && !mbar_wait_warp(&v_full[st], (i >> 1) & 1, abort_flag)) ||
-                            !mbar_wait_warp(&p_full[half], i & 1, abort_flag)) {
+                    }
+                    if (last >= 0) {
+                        const int i = own - 1;
+                        if (!wait_warp(p_full, i & 1, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         if (leader) {
+                            const uint64_t dv = dk0 + last * kStep + (L::kTile >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_ts(tmem + L::kColO, tmem + L::kColP + 32 * half + 8 * kk,
-                                        dv0 + st * kStep + (uint64_t)(half * (8192 >> 4) + kk * 2), kIdescPV,
-                                        n > 1 || half > 0 || kk > 0);
-                            if (half == 1) umma_commit(&v_empty[st]);
-                            umma_commit(&pv_done[half]);
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_ts(tO, tP + 8 * kk, dv + (uint64_t)((kk >> 2) * (8192 >> 4) + (kk & 3) * 2),
+                                        kIdescPV, i > first_own || kk > 0);
+                            umma_commit(&kv_empty[last]);
+                            umma_commit(pv_done);
                         }
                         __syncwarp();
                     }
+                    if (mine) {
+                        last = st;
+                        ++own;
+                    }
                 }
+                if (!ok) break;
+                it += n_tiles;
             }
-            if (!ok) break;
-            it += n_tiles;
-            ++seg;
-        }
-        // every product (and its commits) is finished before TMEM is released
-        if (any_mma) {
-            if (leader) umma_commit(drain_bar);
-            __syncwarp();
-            tc::drain_wait(drain_bar, 0);
-        }
+            // every product (and its commits) is finished before TMEM is released
+            if (any_mma) {
+                if (leader) umma_commit(drain_bar);
+                __syncwarp();
+                tc::drain_wait(drain_bar, 0);
+            }
         }
     } else {
         // ------------------------------------------------------------------ softmax
         setmaxnreg_inc<L::kRegsSoftmax>();
-        const int r = threadIdx.x;
-        const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-        const uint32_t tS = tmem + L::kColS + lane_off, tP = tmem + L::kColP + lane_off, tO = tmem + L::kColO + lane_off;
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const uint32_t tS = tmem + L::colS(half) + lane_off, tP = tmem + L::colP(half) + lane_off,
+                       tO = tmem + L::colO(half) + lane_off;
         const float mul = a.scale_log2;
         Segment g;
-        int it = 0;
-        bool ok = true, first_seg = true;
+        int it = 0, own = 0, joins = 0, problem = 0;
+        bool ok = true;
         while (ok && walk.next(a, &g)) {
-            const int32_t nv = valid_rows(a, g.sc, g.rt);
-            const int32_t x = g.rt * a.tile_rows + r;
-            const int64_t row = out_row(a, g.s, g.h, x);
-            // the products that read the last Q are done: their scores have been read
+            const bool solo = is_solo(a, g.nv);
+            const int in = solo ? r : 128 * half + r;  // row within the problem
+            const bool valid = in < g.nv;
+            const int32_t x = g.rt * a.tile_rows + in;
+            const int64_t row = valid ? out_row(a, g.s, g.h, x) : 0;
+            // the products that read the last Q are done: their scores have been read (and a half without
+            // tiles of the last problem waits until that has been noticed)
+            if (problem > 0 && !wait_warp(q_seen, (problem - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            ++problem;
             {
-                uint8_t* dst = smem + L::kQ + r * 128;
+                uint8_t* dst = smem + L::kQ + half * L::kTile + r * 128;
                 const uint4* src = reinterpret_cast<const uint4*>(a.q + row * 64);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint4 v = r < nv ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+                    const uint4 v = valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(dst + ((j ^ (r & 7)) << 4)) = v;
                 }
             }
             fence_proxy_async_smem();
-            if (r == 0) *seg_tiles = g.t1 - g.t0;
+            const int n_tiles = g.t1 - g.t0;
+            if (r == 0) {
+                seg[0] = n_tiles;
+                seg[1] = solo;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            const int32_t lim = r < nv ? key_limit(a, g.sc, x / a.group) : g.sc.len;
+            const int32_t lim = valid ? key_limit(a, g.sc, x / a.group) : g.sc.len;
             const int32_t least = __reduce_min_sync(0xffffffffu, lim);
             float m_run = -INFINITY, l_run = 0.0f;
-            for (int t = g.t0; t < g.t1; ++t, ++it) {
-                if (!mbar_wait_warp(s_full, it & 1, abort_flag)) {
+            const int first = solo ? half : 0, step = solo ? 2 : 1, first_own = own;
+            for (int n = first; n < n_tiles; n += step, ++own) {
+                const int t = g.t0 + n, st = (it + n) % L::kStages;
+                if (!wait_warp(s_full, own & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                uint32_t sv[128];
+                uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 0);
+                uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32);
+                uint32_t(&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 64);
+                uint32_t(&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 96);
+                tmem_ld_32x32b_x32(tS, s0);
+                tmem_ld_32x32b_x32(tS + 32, s1);
+                tmem_ld_32x32b_x32(tS + 64, s2);
+                tmem_ld_32x32b_x32(tS + 96, s3);
                 // one byte per sub-page; those of this tile's sub-pages were written
-                const uint2 bad8 = ld_shared_v2(smem + L::kBad + (it & 3) * 8);
+                const uint2 bad8 = ld_shared_v2(smem + L::kBad + st * 8);
                 const int subs = 128 >> a.page_log2;
                 const bool bad = (bad8.x & (subs >= 4 ? ~0u : (1u << (8 * subs)) - 1u)) != 0 || (subs == 8 && bad8.y != 0);
-                const bool masked = (int64_t)t * 128 + 128 > least || bad;
-                const int32_t keys = min(max(lim - t * 128, 0), 128);
+                tmem_ld_wait(s0);
+                reg_fence(s1);
+                reg_fence(s2);
+                reg_fence(s3);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+                if ((int64_t)t * 128 + 128 > least || bad) {
+                    const int32_t keys = min(max(lim - t * 128, 0), 128);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int k0 = min(max(keys - 16 * c, 0), 16);
+                        uint32_t seen = (1u << k0) - 1u;
+                        if (bad && bad_pages[st * 8 + ((16 * c) >> a.page_log2)]) seen = 0;
+#pragma unroll
+                        for (int u = 0; u < 16; ++u)
+                            if (!((seen >> u) & 1u)) sv[16 * c + u] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float m8[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) m8[u] = __uint_as_float(sv[u]);
+#pragma unroll
+                for (int c = 8; c < 120; c += 16)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        m8[u] = fmax3(m8[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 8 + u]));
+#pragma unroll
+                for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], __uint_as_float(sv[120 + u]));
+                const float mx = mul * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                float alpha = 1.0f;
+                if (mx > m_run + 8.0f) {
+                    alpha = ex2_approx(m_run - mx);
+                    m_run = mx;
+                    l_run *= alpha;
+                }
+                const float m_use = m_run == -INFINITY ? 0.0f : m_run;
+                const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-m_use, -m_use);
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int u = 0; u < 32; ++u) {
+                        const float2 xv = __ffma2_rn(make_float2(__uint_as_float(sv[64 * c + 2 * u]),
+                                                                 __uint_as_float(sv[64 * c + 2 * u + 1])),
+                                                     mul2, neg2);
+                        float2 p;
+                        p.x = ex2_approx(xv.x);
+                        p.y = ex2_approx(xv.y);
+                        acc[u & 1] = __fadd2_rn(acc[u & 1], p);
+                        pk[u] = pack_bf16x2(p.x, p.y);
+                    }
+                    if (c == 0 && own > first_own) {
+                        // O may be rescaled, and P's place is free, once the last tile's product is done
+                        if (!wait_warp(pv_done, (own - 1) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (__any_sync(0xffffffffu, alpha != 1.0f)) {
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t tSh = tS + 64 * half;
-                    uint32_t sv[64];
-                    uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv);
-                    uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(sv + 32);
-                    tmem_ld_32x32b_x32(tSh, s0);
-                    tmem_ld_32x32b_x32(tSh + 32, s1);
-                    tmem_ld_wait(s0);
-                    reg_fence(s1);
-                    if (half == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(s_free);
-                    }
-                    if (masked) {
+                            for (int d = 0; d < 64; d += 16) {
+                                uint32_t ov[16];
+                                tmem_ld_32x32b_x16(tO + d, ov);
+                                tmem_ld_wait16(ov);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int col = 64 * half + 16 * c, k0 = min(max(keys - col, 0), 16);
-                            uint32_t seen = (1u << k0) - 1u;
-                            if (bad && bad_pages[(it & 3) * 8 + (col >> a.page_log2)]) seen = 0;
-#pragma unroll
-                            for (int u = 0; u < 16; ++u)
-                                if (!((seen >> u) & 1u)) sv[16 * c + u] = __float_as_uint(-INFINITY);
-                        }
-                    }
-                    float m8[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) m8[u] = __uint_as_float(sv[u]);
-#pragma unroll
-                    for (int c = 8; c < 56; c += 16)
-#pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            m8[u] = fmax3(m8[u], __uint_as_float(sv[c + u]), __uint_as_float(sv[c + 8 + u]));
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) m8[u] = fmaxf(m8[u], __uint_as_float(sv[56 + u]));
-                    const float mx = mul * fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-                    if (__any_sync(0xffffffffu, mx > m_run + 8.0f)) {
-                        // raise the maximum of the rows that need it and rescale what was summed, once every
-                        // product so far is done
-                        const float m_new = mx > m_run + 8.0f ? mx : m_run;
-                        const float alpha = m_new == m_run ? 1.0f : ex2_approx(m_run - m_new);
-                        m_run = m_new;
-                        l_run *= alpha;
-                        if (t > g.t0 || half > 0) {
-                            // the half before: of this tile, or the second one of the tile before
-                            if (!mbar_wait_warp(&pv_done[half ^ 1], (half ? it : it - 1) & 1, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < 64; c += 8) {
-                                uint32_t ov[8];
-                                tmem_ld_32x32b_x8(tO + c, ov);
-                                tmem_ld_wait8(ov);
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
-                                tmem_st_32x32b_x8(tO + c, ov);
+                                for (int u = 0; u < 16; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * alpha);
+                                tmem_st_32x32b_x16(tO + d, ov);
                             }
                         }
                     }
-                    const float m_use = m_run == -INFINITY ? 0.0f : m_run;
-                    const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-m_use, -m_use);
-                    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) {
-                            const float2 xv = __ffma2_rn(make_float2(__uint_as_float(sv[32 * c + 2 * u]),
-                                                                     __uint_as_float(sv[32 * c + 2 * u + 1])),
-                                                         mul2, neg2);
-                            float2 p;
-                            p.x = ex2_approx(xv.x);
-                            p.y = ex2_approx(xv.y);
-                            acc = __fadd2_rn(acc, p);
-                            pk[u] = pack_bf16x2(p.x, p.y);
-                        }
-                        // this half's place for P is free once its product of the tile before is done
-                        if (c == 0 && t > g.t0) {
-                            if (!mbar_wait_warp(&pv_done[half], (it - 1) & 1, abort_flag)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-                        tmem_st_32x32b_x16(tP + 32 * half + 16 * c, pk);
-                    }
-                    if (!ok) break;
-                    l_run += acc.x + acc.y;
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[half]);
+                    tmem_st_32x32b_x32(tP + 32 * c, pk);
                 }
                 if (!ok) break;
+                const float2 sum = __fadd2_rn(acc[0], acc[1]);
+                l_run += sum.x + sum.y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
             }
-            if (!ok || !mbar_wait_warp(&pv_done[1], (it - 1) & 1, abort_flag)) {
+            it += n_tiles;
+            const bool any = own > first_own;  // a solo half may have none of a single tile
+            if (!ok || (any && !wait_warp(pv_done, (own - 1) & 1, abort_flag))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-            const int slot = part_slot(first_seg);
-            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t ov[32];
-                tmem_ld_32x32b_x32(tO + 32 * c, ov);
-                tmem_ld_wait(ov);
-                if (r < nv) {
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + row * 64 + 32 * c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                w[u] = pack_bf16x2(__uint_as_float(ov[8 * j + 2 * u]) * inv,
-                                                   __uint_as_float(ov[8 * j + 2 * u + 1]) * inv);
-                            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((int64_t)slot * a.tile_rows + r) * 64 + 32 * c);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+            float* join = reinterpret_cast<float*>(smem + L::kJoin) + r;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (solo) {
+                // half 1 hands its part to half 0
+                if (half == 1) {
+                    if (!wait_warp(x_empty, (joins & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
                     }
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t ov[16];
+                        tmem_ld_32x32b_x16(tO + c, ov);
+                        tmem_ld_wait16(ov);
+#pragma unroll
+                        for (int u = 0; u < 16; ++u) join[128 * (c + u)] = any ? __uint_as_float(ov[u]) : 0.0f;
+                    }
+                    join[128 * 64] = m_run;
+                    join[128 * 65] = l_run;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(x_full);
+                    ++joins;
+                    continue;
+                }
+                if (!wait_warp(x_full, joins & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const float m1 = join[128 * 64], l1 = join[128 * 65];
+                const float mm = fmaxf(m_run, m1), mu = mm == -INFINITY ? 0.0f : mm;
+                f0 = ex2_approx(m_run - mu);
+                f1 = ex2_approx(m1 - mu);
+                l_run = l_run * f0 + l1 * f1;
+                m_run = mm;
+            }
+            const bool whole = g.whole();
+            const int64_t part = (int64_t)g.slot() * a.tile_rows + in;
+            const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+                uint32_t ov[16];
+                tmem_ld_32x32b_x16(tO + c, ov);
+                tmem_ld_wait16(ov);
+                if (solo) {
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        ov[u] = __float_as_uint(__uint_as_float(ov[u]) * f0 + join[128 * (c + u)] * f1);
+                }
+                if (valid && whole) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        w[u] = pack_bf16x2(__uint_as_float(ov[2 * u]) * inv, __uint_as_float(ov[2 * u + 1]) * inv);
+                    uint4* dst = reinterpret_cast<uint4*>(a.o + row * 64 + c);
+                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                } else if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * 64 + c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        dst[j] = make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
                 }
             }
-            if (r < nv) {
+            if (valid) {
                 if (!whole) {
-                    a.part_ml[(int64_t)slot * 2 * a.tile_rows + r] = m_run;
-                    a.part_ml[((int64_t)slot * 2 + 1) * a.tile_rows + r] = l_run;
+                    float* ml = a.part_ml + (int64_t)g.slot() * 2 * a.tile_rows + in;
+                    ml[0] = m_run;
+                    ml[a.tile_rows] = l_run;
                 } else if (a.lse) {
                     const float m_fin = m_run == -INFINITY ? 0.0f : m_run;
                     a.lse[row] = l_run == 0.0f ? -INFINITY : (m_fin + log2f(l_run)) * 0.69314718055994530942f;
                 }
             }
-            first_seg = false;
+            if (solo) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(x_empty);
+                ++joins;
+            }
         }
-        if (ok) {
-            if (r == 0) *seg_tiles = 0;
+        if (ok && (problem == 0 || wait_warp(q_seen, (problem - 1) & 1, abort_flag))) {
+            if (r == 0) seg[0] = 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
@@ -531,7 +603,7 @@ __global__ void __launch_bounds__(384, 2) kv_tc_kernel(const AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }

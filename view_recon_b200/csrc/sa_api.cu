@@ -1361,11 +1361,11 @@ dim3 kv_rows_grid(const sa_kv_cache* c, int32_t n) {
 }
 
 // Query rows of one problem: all rows of a key head's query heads together, in the smallest tile of
-// the few-rows kernel, or 128 at a time on the tensor cores.
-int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
+// the few-rows kernel, or 256 at a time on the tensor cores.
+int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kv::kPairRows; }
 
 // Largest grids of the attention kernels: what the workspace has room for.
-int kv_max_ctas(int32_t tile_rows) { return tile_rows == 128 ? 320 : 640; }
+int kv_max_ctas(int32_t tile_rows) { return tile_rows == kv::kPairRows ? 160 : 640; }
 
 size_t kv_part_bytes(int32_t tile_rows) {
     return align256((size_t)2 * kv_max_ctas(tile_rows) * tile_rows * 64 * 4);
@@ -1399,9 +1399,8 @@ sa_status kv_launch(void (*kernel)(const kv::AttnArgs), kv::AttnArgs& a, int dev
             }
             if (per_sm < 1) return SA_ERR_UNSUPPORTED;
             if (which == 3) {
-                // two blocks fit an SM by design (registers, shared memory and all of the tensor memory);
-                // the register split needs what it hands out
-                per_sm = 2;
+                // one block has all of an SM's tensor memory; its register split needs what it hands out
+                per_sm = 1;
                 cudaFuncAttributes fa;
                 if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) {
                     cudaGetLastError();
@@ -1561,8 +1560,10 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     a.n_pages = cache->n_pages;
     a.max_pages = cache->max_pages;
     a.frame = frame;
-    a.min_tiles = 1;
+    a.min_units = a.tile_rows == kv::kPairRows ? kv::kPairCost : 1;  // a run as long as one tile holds one's beginning
     a.page_bytes = g.page_bytes;
+    a.page_stride = g.page_bytes * cache->heads;
+    a.page_stride = g.page_bytes * cache->heads;
     const float scale = softmax_scale > 0.0f ? softmax_scale : 0.125f;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int64_t problems = (int64_t)a.scenes * a.row_tiles * a.kv_heads;
