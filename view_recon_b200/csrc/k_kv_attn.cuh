@@ -23,6 +23,7 @@ struct AttnArgs {
     float* lse;            // or null
     float* part_o;         // [2 * ctas][tile_rows][64]
     float* part_ml;        // [2 * ctas][2][tile_rows]: running max (base 2), sum
+    int4* part_rec;        // [ctas][2]: the problem that begins in a CTA's run and goes on in later ones
     int32_t scenes, kv_heads, group, rows;
     int32_t tile_rows, row_tiles;  // query rows per problem, problems per (scene, head)
     int32_t page_log2, n_pages, max_pages, frame;
@@ -150,17 +151,46 @@ __device__ __forceinline__ int32_t find_entry(const AttnArgs& a, int64_t x, int6
     return n;
 }
 
+// Rows of the problems that have no keys at all: O = 0, LSE = -inf.  Every thread of every block.
+__device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
+    const int32_t n = a.scenes * a.row_tiles;
+    for (int32_t e = blockIdx.x; e < n; e += a.ctas) {
+        const int s = e / a.row_tiles, rt = e - s * a.row_tiles;
+        const Scene sc = scene_of(a, s);
+        const int32_t nv = valid_rows(a, sc, rt);
+        if (nv == 0 || key_tiles(a, sc, rt) > 0) continue;
+        for (int32_t i = threadIdx.x; i < nv * a.kv_heads * 8; i += blockDim.x) {
+            const int32_t x = i / 8 % nv, h = i / 8 / nv;
+            const int64_t row = out_row(a, s, h, rt * a.tile_rows + x);
+            reinterpret_cast<uint4*>(a.o + row * 64)[i % 8] = make_uint4(0, 0, 0, 0);
+            if (a.lse && i % 8 == 0) a.lse[row] = -INFINITY;
+        }
+    }
+}
+
 // One problem's share of a CTA's run of key tiles.
 struct Segment {
     int32_t s, rt, h;
     int32_t t0, t1, tiles;  // key tiles [t0, t1) of the problem's `tiles`
     int32_t nv;             // its rows
+    int32_t last;           // the CTA that has its last tile, when this one has its first and not all
     Scene sc;
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
     // Workspace slot of a part: a CTA leaves at most two, one of a problem that began before its run
     // and one of a problem that goes on after it.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1); }
 };
+// Leaves the merge kernel a note of the problem that begins in this CTA and goes on (or of none); the
+// same thread calls it before its first segment (null) and at each.
+__device__ __forceinline__ void note_parts(const AttnArgs& a, const Segment* g) {
+    int4* rec = a.part_rec + 2 * blockIdx.x;
+    if (!g)
+        rec[0] = make_int4(-1, 0, 0, 0);
+    else if (g->last >= 0) {
+        rec[1] = make_int4(g->h, g->nv, 0, 0);
+        rec[0] = make_int4(g->last, g->s, g->rt, 0);
+    }
+}
 // Walks the CTA's run; every role of the CTA makes the same walk.  A tile belongs to the run in which
 // its place in the list (cost by cost) begins.
 struct Walk {
@@ -172,7 +202,7 @@ struct Walk {
         h = (int32_t)(within / one);
         u = within - h * one;
     }
-    __device__ __forceinline__ bool next(const AttnArgs& a, Segment* g) {
+    __device__ __forceinline__ bool next(const AttnArgs& a, const Cut& cut, Segment* g) {
         const int32_t n = a.scenes * a.row_tiles;
         while (left > 0 && e < n) {
             g->s = e / a.row_tiles;
@@ -191,6 +221,9 @@ struct Walk {
             g->h = h;
             g->t0 = (int32_t)((u + cost - 1) / cost);
             g->t1 = (int32_t)((u1 + cost - 1) / cost);
+            // the problem's first tile is at this CTA's end - left + 0, its last one (tiles - 1) costs on
+            const int64_t behind = (int64_t)(g->tiles - 1) * cost - left;
+            g->last = u == 0 && behind >= 0 ? (int32_t)(blockIdx.x + 1 + behind / cut.per) : -1;
             left -= u1 - u;
             u = 0;
             ++h;
@@ -263,6 +296,8 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         *abort_flag = 0;
         fence_barrier_init();
     }
+    if (threadIdx.x == 0) note_parts(a, nullptr);
+    write_empty_rows(a);
     const Cut cut = cut_of(a, red);
     const int64_t x0 = blockIdx.x * cut.per;
     Walk walk;
@@ -281,7 +316,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     if (warp == L::kWarps) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
-        while (ok && walk.next(a, &g)) {
+        while (ok && walk.next(a, cut, &g)) {
             const int32_t* row = a.table + (int64_t)g.s * a.max_pages;
             const int32_t lim = (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len);
             for (int t = g.t0; t < g.t1; ++t, ++it) {
@@ -314,7 +349,8 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         // ---------------------------------------------------------------- products
         const int qg = lane >> 2, qc = lane & 3;
         bool ok = true;
-        while (ok && walk.next(a, &g)) {
+        while (ok && walk.next(a, cut, &g)) {
+            if (threadIdx.x == 0) note_parts(a, &g);
             const int32_t nv = g.nv;
             const int32_t r0 = g.rt * a.tile_rows;
             // Q^T operand: row 8 i + qg, channels 16 qc .. 16 qc + 15
@@ -554,58 +590,32 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 
 // ------------------------------------------------------------------------------ joining the parts
 //
-// One block per (entry, head, 8 rows): rows of a problem that several CTAs shared, and rows of one that
-// has no keys at all.  Four groups of threads sum every fourth part, in
-// order, then the groups in order.
+// One block per CTA of the attention kernel and 32 rows (or the whole tile of rows): the problem that
+// begins in that CTA's run and ends in another's.  A thread sums four channels of a row over the parts,
+// in order; for short tiles of rows groups of threads take every second or fourth part, and the groups
+// are summed in order.
 constexpr int kMergeThreads = 512;
 
 __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs a) {
-    __shared__ int64_t red[kMergeThreads / 32];
-    __shared__ int64_t before_smem;
-    __shared__ float4 acc_smem[4][8][16];
-    __shared__ float ml_smem[4][2][8];
-    const int32_t e = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
-    const int32_t s = e / a.row_tiles, rt = e % a.row_tiles;
-    const Scene sc = scene_of(a, s);
-    const int32_t nv = valid_rows(a, sc, rt), tiles = key_tiles(a, sc, rt);
-    const int grp = threadIdx.x / 128, x = (threadIdx.x / 16) % 8, c4 = threadIdx.x % 16;
-    const int row_in = 8 * blockIdx.y + x;
-    if (8 * (int)blockIdx.y >= nv || tiles == 0) {
-        if (grp == 0 && row_in < nv) {  // rows that see no key
-            const int64_t row = out_row(a, s, h, rt * a.tile_rows + row_in);
-            *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) = make_uint2(0u, 0u);
-            if (a.lse && c4 == 0) a.lse[row] = -INFINITY;
-        }
-        wait_previous_kernel();
-        return;
-    }
-    const Cut cut = cut_of(a, red);
-    // place of this problem's first tile in the list
-    int64_t sum = 0;
-    __syncthreads();
-    for (int32_t y = threadIdx.x; y < e; y += blockDim.x) sum += entry_cost(a, y);
-    sum = warp_sum(sum);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    const int32_t cost = tile_cost(a, nv);
-    if (threadIdx.x == 0) {
-        int64_t b = 0;
-        for (int w = 0; w < kMergeThreads / 32; ++w) b += red[w];
-        before_smem = b + (int64_t)h * tiles * cost;
-    }
-    __syncthreads();
-    const int64_t g0 = before_smem;
-    const int c0 = (int)(g0 / cut.per), c1 = (int)((g0 + (int64_t)(tiles - 1) * cost) / cut.per);
+    __shared__ float4 acc_smem[32][16];
+    __shared__ float ml_smem[2][32];
     wait_previous_kernel();
-    if (c0 == c1) return;  // one CTA had all of it and wrote the rows
+    const int4 r0 = __ldcg(a.part_rec + 2 * blockIdx.x);
+    const int32_t c0 = blockIdx.x, c1 = r0.x;
+    if (c1 < 0) return;
+    const int4 r1 = __ldcg(a.part_rec + 2 * blockIdx.x + 1);
+    const int32_t nv = r1.y, rows = min(a.tile_rows, 32), groups = 32 / rows;
+    const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows, x = rows * blockIdx.y + y % rows;
+    if (rows * (int)blockIdx.y >= nv) return;
     float m = -INFINITY, l = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row_in < nv) {
-        for (int c = c0 + grp; c <= c1; c += 4) {
+    if (x < nv) {
+#pragma unroll 2
+        for (int c = c0 + grp; c <= c1; c += groups) {
             const int64_t slot = 2 * (int64_t)c + (c == c0 ? 1 : 0);
-            const float pm = __ldcg(a.part_ml + slot * 2 * a.tile_rows + row_in);
-            const float pl = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + row_in);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + row_in) * 64 + 4 * c4));
+            const float pm = __ldcg(a.part_ml + slot * 2 * a.tile_rows + x);
+            const float pl = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + x);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + x) * 64 + 4 * c4));
             const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.0f : mn;
             const float f = ex2_approx(m - mu), w = ex2_approx(pm - mu);
             acc.x = acc.x * f + v.x * w;
@@ -616,25 +626,28 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
             m = mn;
         }
     }
-    acc_smem[grp][x][c4] = acc;
-    if (c4 == 0) ml_smem[grp][0][x] = m, ml_smem[grp][1][x] = l;
-    __syncthreads();
-    if (grp != 0 || row_in >= nv) return;
-    for (int y = 1; y < 4; ++y) m = fmaxf(m, ml_smem[y][0][x]);
-    const float mu = m == -INFINITY ? 0.0f : m;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    l = 0.0f;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-        const float w = ex2_approx(ml_smem[y][0][x] - mu);
-        const float4 v = acc_smem[y][x][c4];
-        acc.x += v.x * w;
-        acc.y += v.y * w;
-        acc.z += v.z * w;
-        acc.w += v.w * w;
-        l += ml_smem[y][1][x] * w;
+    if (groups > 1) {
+        acc_smem[y][c4] = acc;
+        if (c4 == 0) ml_smem[0][y] = m, ml_smem[1][y] = l;
+        __syncthreads();
+        if (grp != 0) return;
+        for (int i = 1; i < groups; ++i) m = fmaxf(m, ml_smem[0][i * rows + y]);
+        const float mu = m == -INFINITY ? 0.0f : m;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = 0.0f;
+        for (int i = 0; i < groups; ++i) {
+            const float w = ex2_approx(ml_smem[0][i * rows + y] - mu);
+            const float4 v = acc_smem[i * rows + y][c4];
+            acc.x += v.x * w;
+            acc.y += v.y * w;
+            acc.z += v.z * w;
+            acc.w += v.w * w;
+            l += ml_smem[1][i * rows + y] * w;
+        }
     }
-    const int64_t row = out_row(a, s, h, rt * a.tile_rows + row_in);
+    if (x >= nv) return;
+    const float mu = m == -INFINITY ? 0.0f : m;
+    const int64_t row = out_row(a, r0.y, r1.x, r0.z * a.tile_rows + x);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

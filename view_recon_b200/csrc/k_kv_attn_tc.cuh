@@ -204,6 +204,9 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         *abort_flag = 0;
         fence_barrier_init();
     }
+    // thread 256 is the one that notes this block's parts
+    if (threadIdx.x == 256) note_parts(a, nullptr);
+    write_empty_rows(a);
     const Cut cut = cut_of(a, red);
     const int64_t x0 = blockIdx.x * cut.per;
     Walk walk;
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         // The registers hold the tile that is written next; its page pointers were looked up a tile
         // before it was loaded, and it was loaded a tile before it is written.
         Segment g;
-        bool more = walk.next(a, &g);  // tile t of the problem at hand, up to t1
+        bool more = walk.next(a, cut, &g);  // tile t of the problem at hand, up to t1
         if (more) {
             PageRun run(a, g);
             int32_t t = g.t0, t1 = g.t1;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
             kr.load(a, pk, tid);
             vr.load(a, pv, tid);
             auto advance = [&]() {
-                if (++t == t1 && (more = walk.next(a, &g))) {
+                if (++t == t1 && (more = walk.next(a, cut, &g))) {
                     run = PageRun(a, g);
                     t = g.t0;
                     t1 = g.t1;
@@ -371,7 +374,8 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         Segment g;
         int it = 0, own = 0, joins = 0, problem = 0;
         bool ok = true;
-        while (ok && walk.next(a, &g)) {
+        while (ok && walk.next(a, cut, &g)) {
+            if (threadIdx.x == 256) note_parts(a, &g);
             const bool solo = is_solo(a, g.nv);
             const int in = solo ? r : 128 * half + r;  // row within the problem
             const bool valid = in < g.nv;

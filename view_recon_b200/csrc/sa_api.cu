@@ -1371,6 +1371,8 @@ size_t kv_part_bytes(int32_t tile_rows) {
     return align256((size_t)2 * kv_max_ctas(tile_rows) * tile_rows * 64 * 4);
 }
 
+size_t kv_ml_bytes(int32_t tile_rows) { return align256((size_t)2 * kv_max_ctas(tile_rows) * 2 * tile_rows * 4); }
+
 sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvGeo* g) {
     const sa_status st = kv_geo(c, g);
     if (st != SA_OK) return st;
@@ -1519,7 +1521,7 @@ size_t sa_kv_attn_workspace_size(const sa_kv_cache* cache, int32_t q_heads, int3
     KvGeo g;
     if (kv_attn_check(cache, q_heads, rows, &g) != SA_OK) return 0;
     const int32_t tr = kv_tile_rows((int64_t)rows * (q_heads / cache->heads));
-    return kv_part_bytes(tr) + align256((size_t)2 * kv_max_ctas(tr) * 2 * tr * 4);
+    return kv_part_bytes(tr) + kv_ml_bytes(tr) + (size_t)kv_max_ctas(tr) * 2 * sizeof(int4);
 }
 
 sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_heads, int32_t rows,
@@ -1556,6 +1558,8 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     a.row_tiles = (int32_t)((head_rows + a.tile_rows - 1) / a.tile_rows);
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kv_part_bytes(a.tile_rows));
+    a.part_rec = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + kv_part_bytes(a.tile_rows) +
+                                         kv_ml_bytes(a.tile_rows));
     a.page_log2 = g.page_log2;
     a.n_pages = cache->n_pages;
     a.max_pages = cache->max_pages;
@@ -1573,7 +1577,7 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     // the joining kernel is launched ahead of the attention kernel's end and waits for it itself
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)problems, (unsigned)(a.tile_rows / 8));
+    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((a.tile_rows + 31) / 32));
     cfg.blockDim = dim3(kv::kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
