@@ -114,41 +114,64 @@ __device__ __forceinline__ int64_t entry_cost(const AttnArgs& a, int32_t e) {
     const Scene sc = scene_of(a, s);
     return (int64_t)key_tiles(a, sc, rt) * tile_cost(a, valid_rows(a, sc, rt)) * a.kv_heads;
 }
-// Every thread of the block calls it; `red` is shared memory of one int64 per warp.
-__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int64_t* red) {
-    const int32_t n = a.scenes * a.row_tiles;
-    int64_t sum = 0;
-    for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e);
-    sum = warp_sum(sum);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-    __syncthreads();
-    sum = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += red[w];
-    return Cut{sum, max((sum + a.ctas - 1) / a.ctas, (int64_t)a.min_units)};
+__device__ __forceinline__ int64_t warp_scan(int64_t c) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
+        if (lane >= d) c += y;
+    }
+    return c;
 }
-// The entry that holds place x of the list (x < total), and the place within it.  One warp.
-__device__ __forceinline__ int32_t find_entry(const AttnArgs& a, int64_t x, int64_t* within) {
+// Small dividends take the short division.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+// The CTA's run: cuts the list, and finds the entry in which the run begins and the place within it
+// (entry < 0: nothing to do).  Every thread of the block calls it; every warp comes to the same.  Up to
+// 32 entries are one scan in registers; for more, `red` is shared memory of one int64 per warp.
+struct Start {
+    Cut cut;
+    int64_t left, within;
+    int32_t entry;
+};
+__device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
     const int lane = threadIdx.x & 31;
     const int32_t n = a.scenes * a.row_tiles;
+    Start s;
+    int64_t scan = 0;
+    if (n <= 32) {
+        scan = warp_scan(lane < n ? entry_cost(a, lane) : 0);
+        s.cut.total = __shfl_sync(0xffffffffu, scan, 31);
+    } else {
+        int64_t sum = 0;
+        for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e);
+        sum = warp_sum(sum);
+        if (lane == 0) red[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        s.cut.total = 0;
+        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s.cut.total += red[w];
+    }
+    s.cut.per = max(quotient(s.cut.total + a.ctas - 1, a.ctas), (int64_t)a.min_units);
+    const int64_t x = blockIdx.x * s.cut.per;
+    s.left = min(s.cut.per, s.cut.total - x);
+    s.entry = -1;
+    s.within = 0;
+    if (s.left <= 0) return s;
     int64_t before = 0;
     for (int32_t e0 = 0; e0 < n; e0 += 32) {
-        int64_t c = e0 + lane < n ? entry_cost(a, e0 + lane) : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, c, d);
-            if (lane >= d) c += y;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, before + c > x);
+        if (n > 32) scan = warp_scan(e0 + lane < n ? entry_cost(a, e0 + lane) : 0);
+        const uint32_t past = __ballot_sync(0xffffffffu, before + scan > x);
         if (past) {
             const int first = __ffs(past) - 1;
-            const int64_t prev = __shfl_sync(0xffffffffu, c, max(first - 1, 0));
-            *within = x - before - (first > 0 ? prev : 0);
-            return e0 + first;
+            const int64_t prev = __shfl_sync(0xffffffffu, scan, max(first - 1, 0));
+            s.within = x - before - (first > 0 ? prev : 0);
+            s.entry = e0 + first;
+            break;
         }
-        before += __shfl_sync(0xffffffffu, c, 31);
+        before += __shfl_sync(0xffffffffu, scan, 31);
     }
-    *within = 0;
-    return n;
+    return s;
 }
 
 // Rows of the problems that have no keys at all: O = 0, LSE = -inf.  Every thread of every block.
@@ -196,11 +219,13 @@ __device__ __forceinline__ void note_parts(const AttnArgs& a, const Segment* g) 
 struct Walk {
     int64_t left, u;  // cost still to come, place within the problem at hand
     int32_t e, h;
-    __device__ __forceinline__ void start(const AttnArgs& a, int32_t e0, int64_t within) {
-        e = e0;
-        const int64_t one = entry_cost(a, e0) / a.kv_heads;
-        h = (int32_t)(within / one);
-        u = within - h * one;
+    __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s) : left(s.left), u(0), e(s.entry), h(0) {
+        if (e < 0) return;
+        const int sc = e / a.row_tiles, rt = e - sc * a.row_tiles;
+        const Scene scene = scene_of(a, sc);
+        const int64_t one = (int64_t)key_tiles(a, scene, rt) * tile_cost(a, valid_rows(a, scene, rt));
+        h = (int32_t)quotient(s.within, one);
+        u = s.within - h * one;
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, const Cut& cut, Segment* g) {
         const int32_t n = a.scenes * a.row_tiles;
@@ -223,7 +248,7 @@ struct Walk {
             g->t1 = (int32_t)((u1 + cost - 1) / cost);
             // the problem's first tile is at this CTA's end - left + 0, its last one (tiles - 1) costs on
             const int64_t behind = (int64_t)(g->tiles - 1) * cost - left;
-            g->last = u == 0 && behind >= 0 ? (int32_t)(blockIdx.x + 1 + behind / cut.per) : -1;
+            g->last = u == 0 && behind >= 0 ? (int32_t)(blockIdx.x + 1 + quotient(behind, cut.per)) : -1;
             left -= u1 - u;
             u = 0;
             ++h;
@@ -284,8 +309,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     uint64_t* empty = full + L::kStages;
     volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + L::kMeta);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
-    int64_t* walk_smem = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);   // entry, tile within it
-    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 24);        // one per warp
+    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);  // one per warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -298,17 +322,10 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     }
     if (threadIdx.x == 0) note_parts(a, nullptr);
     write_empty_rows(a);
-    const Cut cut = cut_of(a, red);
-    const int64_t x0 = blockIdx.x * cut.per;
-    Walk walk;
-    walk.left = min(cut.per, cut.total - x0);
-    if (warp == 0 && walk.left > 0) {
-        int64_t within;
-        const int32_t e = find_entry(a, x0, &within);
-        if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
-    }
+    const Start start = find_start(a, red);
+    const Cut cut = start.cut;
+    Walk walk(a, start);
     __syncthreads();
-    if (walk.left > 0) walk.start(a, (int32_t)walk_smem[0], walk_smem[1]);
 
     const int page = 1 << a.page_log2, sub_pages = 128 >> a.page_log2;
     Segment g;
@@ -600,29 +617,46 @@ __global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs 
     __shared__ float4 acc_smem[32][16];
     __shared__ float ml_smem[2][32];
     wait_previous_kernel();
-    const int4 r0 = __ldcg(a.part_rec + 2 * blockIdx.x);
+    const int4 r0 = __ldcg(a.part_rec + 2 * blockIdx.x), r1 = __ldcg(a.part_rec + 2 * blockIdx.x + 1);
     const int32_t c0 = blockIdx.x, c1 = r0.x;
     if (c1 < 0) return;
-    const int4 r1 = __ldcg(a.part_rec + 2 * blockIdx.x + 1);
     const int32_t nv = r1.y, rows = min(a.tile_rows, 32), groups = 32 / rows;
     const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows, x = rows * blockIdx.y + y % rows;
     if (rows * (int)blockIdx.y >= nv) return;
     float m = -INFINITY, l = 0.0f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (x < nv) {
-#pragma unroll 2
-        for (int c = c0 + grp; c <= c1; c += groups) {
-            const int64_t slot = 2 * (int64_t)c + (c == c0 ? 1 : 0);
-            const float pm = __ldcg(a.part_ml + slot * 2 * a.tile_rows + x);
-            const float pl = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + x);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + x) * 64 + 4 * c4));
-            const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.0f : mn;
-            const float f = ex2_approx(m - mu), w = ex2_approx(pm - mu);
-            acc.x = acc.x * f + v.x * w;
-            acc.y = acc.y * f + v.y * w;
-            acc.z = acc.z * f + v.z * w;
-            acc.w = acc.w * f + v.w * w;
-            l = l * f + pl * w;
+        constexpr int kBatch = 6;  // parts whose loads are in flight together: the kernel is all latency
+        for (int c = c0 + grp; c <= c1; c += groups * kBatch) {
+            float pm[kBatch], pl[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int ci = c + i * groups;
+                pm[i] = -INFINITY;
+                pl[i] = 0.0f;
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (ci > c1) continue;
+                const int64_t slot = 2 * (int64_t)ci + (ci == c0 ? 1 : 0);
+                pm[i] = __ldcg(a.part_ml + slot * 2 * a.tile_rows + x);
+                pl[i] = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + x);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + x) * 64 + 4 * c4));
+            }
+            float mn = m;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pm[i]);
+            const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2_approx(m - mu);
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float w = ex2_approx(pm[i] - mu);
+                acc.x += v[i].x * w;
+                acc.y += v[i].y * w;
+                acc.z += v[i].z * w;
+                acc.w += v[i].w * w;
+                l += pl[i] * w;
+            }
             m = mn;
         }
     }

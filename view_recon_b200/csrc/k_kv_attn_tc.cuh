@@ -32,8 +32,8 @@ struct TcLayoutKv {
     static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2;
     static constexpr int kBad = kBars + 8 * kNumBars;      // [stage][8 sub-pages] bytes
     static constexpr int kSeg = kBad + 8 * kStages;        // per half: tiles of the problem at hand, solo flag
-    static constexpr int kMisc = kSeg + 16;                // abort flag, tmem base, walk[2], reduction[16]
-    static constexpr int kJoin = kMisc + 8 + 16 + 128;     // solo: half 1's O [64][128 rows], max, sum (f32)
+    static constexpr int kMisc = kSeg + 16;                // abort flag, tmem base, reduction[16]
+    static constexpr int kJoin = kMisc + 8 + 128;     // solo: half 1's O [64][128 rows], max, sum (f32)
     static constexpr int kEnd = kJoin + 66 * 128 * 4;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t colS(int x) { return 256 * x; }
@@ -181,8 +181,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     volatile int* seg = reinterpret_cast<volatile int*>(smem + L::kSeg) + 2 * half;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(smem + L::kMisc + 4);
-    int64_t* walk_smem = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);
-    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 24);
+    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kStages; ++i) {
@@ -207,26 +206,21 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     // thread 256 is the one that notes this block's parts
     if (threadIdx.x == 256) note_parts(a, nullptr);
     write_empty_rows(a);
-    const Cut cut = cut_of(a, red);
-    const int64_t x0 = blockIdx.x * cut.per;
-    Walk walk;
-    walk.left = min(cut.per, cut.total - x0);
-    if (walk.left <= 0) {  // the whole block: nothing to do
+    const Start start = find_start(a, red);
+    const Cut cut = start.cut;
+    if (start.entry < 0) {  // the whole block: nothing to do
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
     if (warp == 0) {
-        int64_t within;
-        const int32_t e = find_entry(a, x0, &within);
-        if (lane == 0) walk_smem[0] = e, walk_smem[1] = within;
         tmem_alloc(tmem_base_smem, L::kTmemCols);
         tmem_relinquish();
     }
+    Walk walk(a, start);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
-    walk.start(a, (int32_t)walk_smem[0], walk_smem[1]);
 
     if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------------ decode

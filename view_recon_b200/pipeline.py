@@ -12,6 +12,7 @@ every step runs in libsa's kernels.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 
 from . import sa
@@ -343,8 +344,11 @@ class DenseAttention:
         return self.o, self.lse
 
 
-def _want(name, t, shape, dtypes, device):
-    """Refuse a tensor that is not of this shape, one of these types, contiguous and on this device."""
+def _want(name, t, shape, dtypes, device, align=16):
+    """Refuse a tensor that is not of this shape, one of these types, contiguous, aligned and on this device;
+    returns its address.  (Calls of a few microseconds: the common case is one line of cheap tests.)"""
+    if t.shape == shape and t.dtype in dtypes and t.device == device and t.is_contiguous() and t.data_ptr() % align == 0:
+        return t.data_ptr()
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.dtype not in dtypes:
@@ -353,13 +357,7 @@ def _want(name, t, shape, dtypes, device):
         raise ValueError("%s is on %s, the cache is on %s" % (name, t.device, device))
     if not t.is_contiguous():
         raise ValueError("%s is not contiguous" % name)
-    if t.data_ptr() % (16 if t.dtype != _int32() else 4):
-        raise ValueError("%s does not start on a 16-byte boundary" % name)
-
-
-def _int32():
-    import torch
-    return torch.int32
+    raise ValueError("%s does not start on a %d-byte boundary" % (name, align))
 
 
 class FrameCache:
@@ -414,6 +412,10 @@ class FrameCache:
             raise ValueError("unsupported cache (head_dim 64, 4 or 8 bits, at least one scene, head and page)")
         self.scenes, self.heads, self.n_pages, self.max_pages = scenes, heads, n_pages, max_pages
         self.page, self.bits, self.d, self.device = page, bits, head_dim, device
+        import torch
+        self._ref = ctypes.byref(self.desc)
+        self._types = (torch.bfloat16, torch.float32)
+        self._count = (torch.int32,)
 
     @classmethod
     def wrap(cls, pool, page_table, lens, page: int = 128, bits: int = 4, head_dim: int = 64) -> "FrameCache":
@@ -427,8 +429,8 @@ class FrameCache:
                     pool.device)
         per_page = c.pool_bytes // (c.n_pages * c.heads)
         _want("pool", pool, (c.n_pages, c.heads, per_page), (torch.uint8,), pool.device)
-        _want("page_table", page_table, (c.scenes, c.max_pages), (torch.int32,), pool.device)
-        _want("lens", lens, (c.scenes,), (torch.int32,), pool.device)
+        _want("page_table", page_table, (c.scenes, c.max_pages), (torch.int32,), pool.device, 4)
+        _want("lens", lens, (c.scenes,), (torch.int32,), pool.device, 4)
         c.pool, c.page_table, c.lens, c._owner = pool, page_table, lens, False
         return c
 
@@ -475,40 +477,48 @@ class FrameCache:
         self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
 
     # ---- rows (each one C call)
-    def _rows(self, name, t, shape, dtypes):
-        _want(name, t, shape, dtypes, self.device)
-
     def _counts(self, name, t):
-        if t is not None:
-            import torch
-            _want(name, t, (self.scenes,), (torch.int32,), self.device)
+        return None if t is None else _want(name, t, (self.scenes,), self._count, self.device, 4)
+
+    def _call(self, fn, *args, stream):
+        """One C call on the cache's device, on `stream` or the device's current one."""
+        import torch
+        index = self.device.index
+        if torch.cuda.current_device() == index:
+            st = fn(self._ref, *args, sa.raw_stream(index, stream))
+        else:
+            with torch.cuda.device(index):
+                st = fn(self._ref, *args, sa.raw_stream(index, stream))
+        if st != sa.SA_OK:
+            raise sa.SaError(fn.__name__, st, sa.status_string(st))
 
     def append(self, k, v, new_len=None, stream=None):
         """Write rows k, v [scenes * heads][n][64] (bf16 or f32) as the last n tokens of every scene; with
         new_len (int32 device tensor [scenes]) only the first new_len[s] rows, as the last new_len[s] tokens."""
-        import torch
-        shape = (self.scenes * self.heads, k.shape[1] if k.dim() == 3 else -1, self.d)
-        self._rows("k", k, shape, (torch.bfloat16, torch.float32))
-        self._rows("v", v, shape, (k.dtype,))
-        self._counts("new_len", new_len)
-        with torch.cuda.device(self.device):
-            sa.sa_kv_append(self.desc, k, v, shape[1], new_len, self.lens, self.page_table, self.pool, stream)
+        n = k.shape[1] if k.dim() == 3 else -1
+        shape = (self.scenes * self.heads, n, self.d)
+        pk = _want("k", k, shape, self._types, self.device)
+        pv = _want("v", v, shape, (k.dtype,), self.device)
+        if n == 0:
+            return
+        self._call(sa.load().sa_kv_append, sa.SA_BF16 if k.dtype is self._types[0] else sa.SA_F32, pk, pv, n,
+                   self._counts("new_len", new_len), self.lens.data_ptr(), self.page_table.data_ptr(),
+                   self.pool.data_ptr(), stream=stream)
 
     def read(self, k=None, v=None, start=None, n_len=None, stream=None):
         """Fill k and v [scenes * heads][n][64] (bf16 or f32, either may be None) with the tokens from start[s]
         (default: the last n, or n_len[s], of each scene); returns (k, v)."""
-        import torch
         ref = k if k is not None else v
         if ref is None:
             raise ValueError("nothing to read into")
-        shape = (self.scenes * self.heads, ref.shape[1] if ref.dim() == 3 else -1, self.d)
-        for name, t in (("k", k), ("v", v)):
-            if t is not None:
-                self._rows(name, t, shape, (torch.bfloat16, torch.float32) if t is ref else (ref.dtype,))
-        self._counts("start", start)
-        self._counts("n_len", n_len)
-        with torch.cuda.device(self.device):
-            sa.sa_kv_read(self.desc, shape[1], n_len, start, self.lens, self.page_table, self.pool, k, v, stream)
+        n = ref.shape[1] if ref.dim() == 3 else -1
+        shape = (self.scenes * self.heads, n, self.d)
+        pk = None if k is None else _want("k", k, shape, self._types, self.device)
+        pv = None if v is None else _want("v", v, shape, self._types if k is None else (k.dtype,), self.device)
+        if n:
+            self._call(sa.load().sa_kv_read, sa.SA_BF16 if ref.dtype is self._types[0] else sa.SA_F32, n,
+                       self._counts("n_len", n_len), self._counts("start", start), self.lens.data_ptr(),
+                       self.page_table.data_ptr(), self.pool.data_ptr(), pk, pv, stream=stream)
         return k, v
 
 
@@ -532,6 +542,7 @@ class CachedGlobalAttention:
         if nbytes == 0:
             raise ValueError("q_heads is a multiple of the cache's heads and rows is positive")
         bh, dev = cache.scenes * self.q_heads, cache.device
+        self._q_shape = (bh, self.rows, cache.d)
         self.ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
         self.o = torch.zeros((bh, self.rows, cache.d), dtype=torch.bfloat16, device=dev)
         self.lse = torch.zeros((bh, self.rows), dtype=torch.float32, device=dev) if with_lse else None
@@ -539,13 +550,11 @@ class CachedGlobalAttention:
     def forward(self, q, q_len=None, stream=None):
         """q [scenes * q_heads][rows][64] bf16; with q_len (int32 device tensor [scenes]) only the first q_len[s]
         rows of scene s.  Returns the (O, LSE) buffers; rows past q_len[s] keep what they held."""
-        import torch
         c = self.cache
-        _want("q", q, (c.scenes * self.q_heads, self.rows, c.d), (torch.bfloat16,), c.device)
-        c._counts("q_len", q_len)
-        with torch.cuda.device(c.device):
-            sa.sa_kv_attn_fwd(c.desc, q, self.q_heads, self.rows, q_len, self.frame, self.softmax_scale, c.lens,
-                              c.page_table, c.pool, self.ws, self.o, self.lse, stream)
+        pq = _want("q", q, self._q_shape, c._types[:1], c.device)
+        c._call(sa.load().sa_kv_attn_fwd, pq, self.q_heads, self.rows, c._counts("q_len", q_len), self.frame,
+                self.softmax_scale, c.lens.data_ptr(), c.page_table.data_ptr(), c.pool.data_ptr(), self.ws.data_ptr(),
+                self.ws.numel(), self.o.data_ptr(), None if self.lse is None else self.lse.data_ptr(), stream=stream)
         return self.o, self.lse
 
     __call__ = forward

@@ -299,6 +299,17 @@ def _dtype_of(t) -> int:
     raise ValueError("expected a bf16 or f32 tensor")
 
 
+def raw_stream(device_index: int, stream=None) -> int:
+    """Handle of a torch stream, or of the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    except AttributeError:  # the same, through a Stream object
+        return torch.cuda.current_stream(device_index).cuda_stream
+
+
 def sa_kv_pool_size(cache: SaKvCache) -> int:
     return int(load().sa_kv_pool_size(ctypes.byref(cache)))
 
