@@ -102,6 +102,7 @@ struct CacheArgs {
     int32_t scenes, heads, n;
     int32_t page_log2, n_pages, max_pages;
     int64_t page_bytes;     // bytes of one page of one head
+    int32_t wide;           // k and v start on 32-byte boundaries: whole sectors a lane and access
 };
 
 // Tokens of a scene, clamped to what its row of the page table can hold (reported when it is not).
@@ -125,55 +126,73 @@ __device__ __forceinline__ int32_t scene_rows(const int32_t* n_len, int s, int32
     return m;
 }
 
+// 32 bytes of a row, as one access where the address allows it: with two of 16 bytes every lane's
+// sector is touched twice (half a sector a store cost the reading kernel a quarter of its rate).
+__device__ __forceinline__ void load32(const void* p, int wide, uint32_t* w) {
+    if (wide) {
+        asm volatile("ld.global.cs.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldcs(static_cast<const uint4*>(p)), b = __ldcs(static_cast<const uint4*>(p) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store32(void* p, int wide, const uint32_t* w) {
+    if (wide) {
+        asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        __stcs(static_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(static_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
 // --------------------------------------------------------------------------- writing
 
+// 16 channels of one row as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load16(const T* src, float (&x)[16]);
-template <>
-__device__ __forceinline__ void load16<float>(const float* src, float (&x)[16]) {
+struct Raw {
+    static constexpr int kWords = 4 * sizeof(T);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* src, int wide) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(src) + i);
-        x[4 * i] = q.x;
-        x[4 * i + 1] = q.y;
-        x[4 * i + 2] = q.z;
-        x[4 * i + 3] = q.w;
+        for (int i = 0; i < kWords; i += 8) load32(reinterpret_cast<const uint32_t*>(src) + i, wide, w + i);
     }
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* src, float (&x)[16]) {
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 q = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
     }
-}
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
 
-// Quantises 16 channels: integer codes (4 bits: code + 8; 8 bits: signed) and the scale byte.
-// x / s is decided exactly.  A product with the rounded reciprocal of s is within 2^-22 of it; what
-// rounding can get wrong is a value on, or next to, the border m + 1/2 between two codes.
-//   8 bits: s is a power of two, the product is exact.
-//   bf16 x: x / s is a border exactly or at least 1e-3 off it (8-bit x, 4-bit s), so rounding the
-//     product to a multiple of 2^-14 first (adding and subtracting 1.5 * 2^9) restores the tie.
-//   f32 x: the remainder x - m s is exact (one FMA; it has at most the bits of x) and moves m where
-//     it is over s / 2, or a tie that rounded to odd.
+// max(|a|, |b|, |c|), NaN if one of them is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// x limited to [-top, top] in one instruction: the smaller magnitude with x's sign
+__device__ __forceinline__ float limit_abs(float x, float top) {
+    float d;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(top));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float c) { return __fadd2_rn(a, make_float2(c, c)); }
+
+// Scale byte of 16 channels; replaces what cannot be stored (infinities become the largest stored
+// magnitude, NaN zero) and reports it.
 template <int BITS, typename T>
-__device__ __forceinline__ uint32_t quantise16(float (&x)[16], int32_t (&code)[16]) {
-    constexpr bool kBf16 = sizeof(T) == 2;
-    constexpr float kTop = BITS == 4 ? 7.0f : 127.0f;
-    float most = 0.0f, bad = 0.0f;
+__device__ __forceinline__ int32_t scale_byte(float (&x)[16]) {
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        most = fmaxf(most, fabsf(x[i]));
-        bad = fmaf(x[i], 0.0f, bad);  // NaN once any x is infinite or NaN
-    }
-    if (!(bad == 0.0f)) {
-        // no code stands for them: infinities become the largest stored magnitude, NaN zero
+    for (int i = 0; i < 16; i += 2) most = max_abs3(most, x[i], x[i + 1]);
+    if (!(most <= 3.402823466e38f)) {
         sa_flag_error(SA_ERR_NONFINITE);
         most = 0.0f;
 #pragma unroll
@@ -182,55 +201,105 @@ __device__ __forceinline__ uint32_t quantise16(float (&x)[16], int32_t (&code)[1
             most = fmaxf(most, fabsf(x[i]));
         }
     }
-    int32_t b;
     if constexpr (BITS == 4) {
-        // truncated to 4 significant bits it is the scale sought or the one or two below it
-        b = (int32_t)(__float_as_uint(most * (1.0f / 7.5f)) >> 20);
+        // truncated to 4 significant bits, most / 7.5 is the scale sought or the one below it (or, when an
+        // f32 quotient rounded down across a scale, the second below)
+        int32_t b = (int32_t)(__float_as_uint(most * (1.0f / 7.5f)) >> 20);
         b += 7.5f * __uint_as_float((uint32_t)b << 20) < most;
-        b += 7.5f * __uint_as_float((uint32_t)b << 20) < most;
-        b = min(max(b - (int32_t)(kScaleF32Bits >> 20), 0), 255);
+        if (sizeof(T) == 4) b += 7.5f * __uint_as_float((uint32_t)b << 20) < most;
+        return min(max(b - (int32_t)(kScaleF32Bits >> 20), 0), 255);
     } else {
         int32_t e = (int32_t)(__float_as_uint(most * (1.0f / 127.5f)) >> 23);
         e += 127.5f * __uint_as_float((uint32_t)e << 23) < most;
         e += 127.5f * __uint_as_float((uint32_t)e << 23) < most;
-        b = 8 * min(max(e - (127 - kScaleBias), 0), 31);
+        return 8 * min(max(e - (127 - kScaleBias), 0), 31);
     }
-    const float s = __uint_as_float(((uint32_t)b << 20) + kScaleF32Bits);
-    const float inv = __frcp_rn(s);
+}
+
+// Codes (as whole floats) of pairs of channels: n.x of a channel with scale s.x, n.y of one with s.y.
+// x / s is decided exactly.  A product with the reciprocal of s is within 2^-21 of it; what rounding can
+// get wrong is a value on, or next to, the border m + 1/2 between two codes.
+//   8 bits: s is a power of two, the product is exact.
+//   bf16 x: x / s is a border exactly or at least 1e-3 off it (8-bit x, 4-bit s), so rounding the
+//     product to a multiple of 2^-14 first (adding and subtracting 1.5 * 2^9) restores the tie.
+//   f32 x: the remainder x - n s is exact (one FMA; it has at most the bits of x).  Where none of a
+//     thread's 16 reaches s / 2, which is nearly always, all are right; otherwise n moves where the
+//     remainder is over s / 2, or is s / 2 and n is odd.
+struct PairScale {
+    float2 s, inv;
+};
+template <int BITS>
+__device__ __forceinline__ PairScale pair_scale(int32_t bx, int32_t by) {
+    PairScale p;
+    p.s = make_float2(__uint_as_float(((uint32_t)bx << 20) + kScaleF32Bits),
+                      __uint_as_float(((uint32_t)by << 20) + kScaleF32Bits));
+    if constexpr (BITS == 4) {
+        p.inv = make_float2(__frcp_rn(p.s.x), __frcp_rn(p.s.y));
+    } else {
+        p.inv = make_float2(__uint_as_float((254u << 23) - __float_as_uint(p.s.x)),
+                            __uint_as_float((254u << 23) - __float_as_uint(p.s.y)));
+    }
+    return p;
+}
+template <int BITS, typename T, int N>
+__device__ __forceinline__ void round_codes(const float2 (&x)[N], const PairScale& p, float2 (&n)[N]) {
+    constexpr float kTop = BITS == 4 ? 7.0f : 127.0f;
+    float worst = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float u = fminf(fmaxf(x[i] * inv, -kTop), kTop);
-        float m;
-        if constexpr (BITS == 4 && kBf16) {
-            u = __fadd_rn(__fadd_rn(u, 768.0f), -768.0f);
-            m = u;
-        } else if constexpr (BITS == 4) {
-            float n = rintf(u);
-            const float d = fmaf(-n, s, x[i]);
-            const float over = fabsf(d) - 0.5f * s;
-            if (over > 0.0f || (over == 0.0f && ((int)n & 1))) n += d > 0.0f ? 1.0f : -1.0f;
-            m = fminf(fmaxf(n, -kTop), kTop);
-        } else {
-            m = u;
+    for (int i = 0; i < N; ++i) {
+        float2 u = __fmul2_rn(x[i], p.inv);
+        u.x = limit_abs(u.x, kTop);
+        u.y = limit_abs(u.y, kTop);
+        if (BITS == 4 && sizeof(T) == 2) u = add2(add2(u, 768.0f), -768.0f);
+        // adding and subtracting 1.5 * 2^23 rounds to the nearest integer, ties to even
+        n[i] = add2(add2(u, 12582912.0f), -12582912.0f);
+        if (BITS == 4 && sizeof(T) == 4) {
+            const float2 d = __ffma2_rn(make_float2(-n[i].x, -n[i].y), p.s, x[i]);
+            worst = max_abs3(worst, d.x * p.inv.x, d.y * p.inv.y);
         }
-        // adding 1.5 * 2^23 rounds to the nearest integer, ties to even
-        code[i] = (int32_t)__float_as_uint(__fadd_rn(m, 12582912.0f)) - (BITS == 4 ? 0x4B400000 - 8 : 0x4B400000);
     }
-    return (uint32_t)b;
+    if (BITS == 4 && sizeof(T) == 4 && worst >= 0.49999f) {
+        auto settle = [&](float x1, float s1, float& n1) {
+            const float d = fmaf(-n1, s1, x1), over = fabsf(d) - 0.5f * s1;
+            if (over > 0.0f || (over == 0.0f && ((int)n1 & 1))) n1 += d > 0.0f ? 1.0f : -1.0f;
+            n1 = fminf(fmaxf(n1, -kTop), kTop);
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            settle(x[i].x, p.s.x, n[i].x);
+            settle(x[i].y, p.s.y, n[i].y);
+        }
+    }
+}
+// The two units of a word from 16 / BITS code pairs (pair.x for the low unit, pair.y for the high one):
+// 4 bits: sum of (code + 8) 16^j in f32, exact below 2^16; 2^23 more leaves it in the low bits
+template <int BITS>
+__device__ __forceinline__ uint32_t pack_word(const float2* n) {
+    if constexpr (BITS == 4) {
+        float2 v = add2(n[0], 8388608.0f + 8.0f * 4369.0f);
+        v = __ffma2_rn(n[1], make_float2(16.0f, 16.0f), v);
+        v = __ffma2_rn(n[2], make_float2(256.0f, 256.0f), v);
+        v = __ffma2_rn(n[3], make_float2(4096.0f, 4096.0f), v);
+        return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x5410);
+    } else {
+        const float2 v = __ffma2_rn(make_float2(fabsf(n[1].x), fabsf(n[1].y)), make_float2(256.0f, 256.0f),
+                                    make_float2(fabsf(n[0].x) + 8388608.0f, fabsf(n[0].y) + 8388608.0f));
+        const uint32_t mag = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x5410);
+        // signs: bytes 3 of n[1].x, n[0].x, n[1].y, n[0].y in bytes 0 to 3
+        const uint32_t lo = __byte_perm(__float_as_uint(n[1].x), __float_as_uint(n[0].x), 0x0073);
+        const uint32_t hi = __byte_perm(__float_as_uint(n[1].y), __float_as_uint(n[0].y), 0x0073);
+        return and_or(__byte_perm(lo, hi, 0x5410), 0x80808080u, mag);
+    }
 }
 
-__device__ __forceinline__ uint32_t unit4(int32_t a, int32_t b, int32_t c, int32_t d) {
-    return (uint32_t)a | (uint32_t)b << 4 | (uint32_t)c << 8 | (uint32_t)d << 12;
-}
-__device__ __forceinline__ uint32_t unit8(int32_t a, int32_t b) {
-    return (uint32_t)abs(a) | (a < 0 ? 0x8000u : 0u) | (uint32_t)abs(b) << 8 | (b < 0 ? 0x80u : 0u);
-}
-
-// One thread: 16 channels of a token pair, K and V.  Whole 16-byte loads (eight in flight a
-// thread for bf16), no shuffles: the maximum of a scale's 16 channels is a thread's own.
+// One thread: 16 channels of a token pair, K and V: the maximum of a scale's 16 channels is a thread's
+// own, and no thread shares a word with another.  Bound by its arithmetic at first (17 instructions an
+// element, 3.0 TB/s of bf16 into 4 bits); packed f32 pairs, three-input maxima and packing by
+// multiply-add leave about 8.
 template <int BITS, typename T>
-__global__ void __launch_bounds__(256) append_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(256, BITS == 4 && sizeof(T) == 2 ? 4 : 3) append_kernel(const CacheArgs a) {
     using F = Fmt<BITS>;
+    constexpr int kPer = 16 / BITS;  // codes of one unit
     const int h = blockIdx.x % a.heads, s = blockIdx.x / a.heads;
     const int32_t n = scene_rows(a.n_len, s, a.n);
     const int32_t len = scene_len(a.lens, s, a.max_pages, a.page_log2);
@@ -249,89 +318,90 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheArgs a) {
             continue;
         }
         const bool live[2] = {t >= lo, t + 1 < len};
-        const T* k = static_cast<const T*>(a.k) + ((int64_t)blockIdx.x * a.n + (t - p0)) * 64 + 16 * blk;
-        const T* v = static_cast<const T*>(a.v) + ((int64_t)blockIdx.x * a.n + (t - p0)) * 64 + 16 * blk;
-        float x[4][16];
+        const int64_t at = ((int64_t)blockIdx.x * a.n + (t - p0)) * 64 + 16 * blk;
+        Raw<T> raw[2][2];  // [K, V][token]
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            raw[0][e].zero();
+            raw[1][e].zero();
             if (live[e]) {
-                load16<T>(k + 64 * e, x[e]);
-                load16<T>(v + 64 * e, x[2 + e]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[e][i] = x[2 + e][i] = 0.0f;
+                raw[0][e].load(static_cast<const T*>(a.k) + at + 64 * e, a.wide);
+                raw[1][e].load(static_cast<const T*>(a.v) + at + 64 * e, a.wide);
             }
         }
         const int32_t slot = t & (page - 1);
         uint8_t* base = a.pool + ((int64_t)pid * a.heads + h) * a.page_bytes;
-        uint8_t* kc = base + slot * F::kDB + blk * (F::kDB / 4);
-        uint8_t* ks = base + page * F::kDB + slot * 4 + blk;
-        uint8_t* vc = base + page * (F::kDB + 4) + (slot / 2) * (2 * F::kDB) + blk * (F::kDB / 2);
-        uint8_t* vs = base + page * (2 * F::kDB + 4) + (slot / 2) * 8 + 2 * blk;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // K: pairs along the channels
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = raw[0][e].get(i);
+            const int32_t b = scale_byte<BITS, T>(x);
+            float2 xp[8], np[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) xp[i] = make_float2(x[2 * i], x[2 * i + 1]);
+            round_codes<BITS, T>(xp, pair_scale<BITS>(b, b), np);
+            if (!live[e]) continue;
+            uint8_t* kc = base + (slot + e) * F::kDB + blk * (F::kDB / 4);
+            uint32_t w[F::kWords];
+#pragma unroll
+            for (int i = 0; i < F::kWords; ++i) w[i] = pack_word<BITS>(np + i * kPer);
+            if constexpr (BITS == 4) *reinterpret_cast<uint2*>(kc) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint4*>(kc) = make_uint4(w[0], w[1], w[2], w[3]);
+            base[page * F::kDB + (slot + e) * 4 + blk] = (uint8_t)b;
+        }
+        // V: pairs along the tokens
+        float x[2][16];
+        int32_t b[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            int32_t c[16];
-            const uint32_t b = quantise16<BITS, T>(x[e], c);
-            if (!live[e]) continue;
-            if constexpr (BITS == 4) {
-                uint2 w;
-                w.x = unit4(c[0], c[2], c[4], c[6]) | unit4(c[1], c[3], c[5], c[7]) << 16;
-                w.y = unit4(c[8], c[10], c[12], c[14]) | unit4(c[9], c[11], c[13], c[15]) << 16;
-                *reinterpret_cast<uint2*>(kc + e * F::kDB) = w;
-            } else {
-                uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = unit8(c[4 * i], c[4 * i + 2]) | unit8(c[4 * i + 1], c[4 * i + 3]) << 16;
-                *reinterpret_cast<uint4*>(kc + e * F::kDB) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            ks[4 * e] = (uint8_t)b;
+            for (int i = 0; i < 16; ++i) x[e][i] = raw[1][e].get(i);
+            b[e] = scale_byte<BITS, T>(x[e]);
         }
-        {
-            constexpr int kUnits = 16 * BITS / 16;  // units of one token's 16 channels
-            uint32_t unit[2][kUnits], b[2];
+        float2 xp[16], np[16];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                int32_t c[16];
-                b[e] = quantise16<BITS, T>(x[2 + e], c);
+        for (int i = 0; i < 16; ++i) xp[i] = make_float2(x[0][i], x[1][i]);
+        round_codes<BITS, T>(xp, pair_scale<BITS>(b[0], b[1]), np);
+        uint8_t* vc = base + page * (F::kDB + 4) + (slot / 2) * (2 * F::kDB) + blk * (F::kDB / 2);
+        uint8_t* vs = base + page * (2 * F::kDB + 4) + (slot / 2) * 8 + 2 * blk;
+        uint32_t w[2 * F::kWords];
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i)
-                    unit[e][i] = BITS == 4 ? unit4(c[4 * i % 16], c[(4 * i + 1) % 16], c[(4 * i + 2) % 16], c[(4 * i + 3) % 16])
-                                           : unit8(c[2 * i], c[2 * i + 1]);
-            }
-            if (live[0] && live[1]) {
+        for (int i = 0; i < 2 * F::kWords; ++i) w[i] = pack_word<BITS>(np + i * kPer);
+        if (live[0] && live[1]) {
 #pragma unroll
-                for (int i = 0; i < kUnits; i += 4)
-                    *reinterpret_cast<uint4*>(vc + 4 * i) =
-                        make_uint4(unit[0][i] | unit[1][i] << 16, unit[0][i + 1] | unit[1][i + 1] << 16,
-                                   unit[0][i + 2] | unit[1][i + 2] << 16, unit[0][i + 3] | unit[1][i + 3] << 16);
-                *reinterpret_cast<uint16_t*>(vs) = (uint16_t)(b[0] | b[1] << 8);
-            } else {
-                const int e = live[1] ? 1 : 0;
+            for (int i = 0; i < 2 * F::kWords; i += 4)
+                *reinterpret_cast<uint4*>(vc + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            *reinterpret_cast<uint16_t*>(vs) = (uint16_t)(b[0] | b[1] << 8);
+        } else {
+            const int e = live[1] ? 1 : 0;
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i)
-                    *reinterpret_cast<uint16_t*>(vc + 4 * i + 2 * e) = (uint16_t)(e ? unit[1][i] : unit[0][i]);
-                vs[e] = (uint8_t)(e ? b[1] : b[0]);
-            }
+            for (int i = 0; i < 2 * F::kWords; ++i)
+                *reinterpret_cast<uint16_t*>(vc + 4 * i + 2 * e) = (uint16_t)(e ? w[i] >> 16 : w[i]);
+            vs[e] = (uint8_t)(e ? b[1] : b[0]);
         }
     }
 }
 
 // --------------------------------------------------------------------------- reading back
 
+// 16 channels as bf16x2 words, in the row's type
 template <typename T>
-__device__ __forceinline__ void store16(T* dst, const uint32_t (&w)[8]);  // w: bf16x2 of 16 channels
-template <>
-__device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* dst, const uint32_t (&w)[8]) {
-    __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-    __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
-}
-template <>
-__device__ __forceinline__ void store16<float>(float* dst, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void store16(T* dst, int wide, const uint32_t (&w)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        store32(dst, wide, w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        __stcs(reinterpret_cast<uint4*>(dst) + i, make_uint4(w[2 * i] << 16, w[2 * i] & 0xFFFF0000u, w[2 * i + 1] << 16,
-                                                             w[2 * i + 1] & 0xFFFF0000u));
+        for (int j = 0; j < 2; ++j) {
+            uint32_t f[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = w[4 * j + i] << 16;
+                f[2 * i + 1] = w[4 * j + i] & 0xFFFF0000u;
+            }
+            store32(dst + 8 * j, wide, f);
+        }
+    }
 }
 
 // One thread: 16 channels of a token pair, K and V (the writing kernel's mapping).
@@ -376,7 +446,7 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheArgs a) {
                 uint32_t out[8];
                 const uint32_t s2 = scale_pair(sb[e] * 0x00010001u);
                 decode<BITS>(w[e], s2, offset_pair<BITS>(s2), out);
-                if (live[e]) store16<T>(static_cast<T*>(a.k) + row + 64 * e, out);
+                if (live[e]) store16<T>(static_cast<T*>(a.k) + row + 64 * e, a.wide, out);
             }
         }
         if (a.v) {
@@ -404,8 +474,8 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheArgs a) {
                     odd[4 * i + j] = __byte_perm(out[2 * j], out[2 * j + 1], 0x7632);
                 }
             }
-            if (live[0]) store16<T>(static_cast<T*>(a.v) + row, even);
-            if (live[1]) store16<T>(static_cast<T*>(a.v) + row + 64, odd);
+            if (live[0]) store16<T>(static_cast<T*>(a.v) + row, a.wide, even);
+            if (live[1]) store16<T>(static_cast<T*>(a.v) + row + 64, a.wide, odd);
         }
     }
 }

@@ -1351,6 +1351,7 @@ sa_status kv_geo(const sa_kv_cache* c, KvGeo* g) {
     return SA_OK;
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Thread blocks of the two row kernels: one column per (scene, head), enough blocks along the rows
@@ -1470,6 +1471,7 @@ sa_status sa_kv_append(const sa_kv_cache* cache, sa_dtype dtype, const void* k, 
     a.n_pages = cache->n_pages;
     a.max_pages = cache->max_pages;
     a.page_bytes = g.page_bytes;
+    a.wide = aligned32(k) && aligned32(v);
     const dim3 grid = kv_rows_grid(cache, n);
     if (cache->bits == 4)
         dtype == SA_BF16 ? kv::append_kernel<4, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
@@ -1507,6 +1509,7 @@ sa_status sa_kv_read(const sa_kv_cache* cache, sa_dtype dtype, int32_t n, const 
     a.n_pages = cache->n_pages;
     a.max_pages = cache->max_pages;
     a.page_bytes = g.page_bytes;
+    a.wide = aligned32(k_or_null) && aligned32(v_or_null);
     const dim3 grid = kv_rows_grid(cache, n);
     if (cache->bits == 4)
         dtype == SA_BF16 ? kv::read_kernel<4, __nv_bfloat16><<<grid, 256, 0, stream>>>(a)
