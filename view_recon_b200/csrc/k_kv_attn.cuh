@@ -365,6 +365,18 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     } else {
         // ---------------------------------------------------------------- products
         const int qg = lane >> 2, qc = lane & 3;
+        // where this lane's codes and scales of its 32 keys are within a stage, 16 keys at a time (a page
+        // holds 16 keys at least)
+        int k_at[2], ks_at[2], v_at[2], vs_at[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int kk = 32 * warp + 16 * u, slot = kk & (page - 1);
+            const int base = L::kRing + (kk >> a.page_log2) * (int)a.page_bytes;
+            k_at[u] = base + (slot + qg) * F::kDB + qc * (F::kDB / 4);
+            ks_at[u] = base + page * F::kDB + (slot + qg) * 4 + qc;
+            v_at[u] = base + page * (F::kDB + 4) + (slot / 2 + qc) * (2 * F::kDB) + qg * (F::kDB / 4);
+            vs_at[u] = base + page * (2 * F::kDB + 4) + (slot / 2 + qc) * 8 + (qg & ~1);
+        }
         bool ok = true;
         while (ok && walk.next(a, cut, &g)) {
             if (threadIdx.x == 0) note_parts(a, &g);
@@ -395,7 +407,8 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
             }
             least = min(least, g.sc.len);
             least = __reduce_min_sync(0xffffffffu, least);
-            float o[NT][4][4], m[NT][2], l[NT][2];
+            float o[NT][4][4], m[NT][2];
+            float2 l[NT];
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 #pragma unroll
                     for (int c = 0; c < 4; ++c) o[i][j][c] = 0.0f;
                 m[i][0] = m[i][1] = -INFINITY;
-                l[i][0] = l[i][1] = 0.0f;
+                l[i] = make_float2(0.0f, 0.0f);
             }
             for (int t = g.t0; t < g.t1; ++t, ++it) {
                 const int st = it % L::kStages;
@@ -411,27 +424,24 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                     ok = false;
                     break;
                 }
-                const uint8_t* ring = smem + L::kRing + st * L::kStageBytes;
+                const uint8_t* ring = smem + st * L::kStageBytes;
                 const int key0 = t * 128 + 32 * warp;  // this warp's keys of the tile
                 if (key0 < g.sc.len) {
                     float sc[NT][2][4];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int kk = 32 * warp + 16 * u, slot = kk & (page - 1);
-                        const uint8_t* base = ring + (kk >> a.page_log2) * a.page_bytes;
                         uint32_t ka[2][8];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int tok = slot + 8 * e + qg;
                             uint32_t w[F::kWords];
-                            const uint2* src = reinterpret_cast<const uint2*>(base + tok * F::kDB + qc * (F::kDB / 4));
+                            const uint2* src = reinterpret_cast<const uint2*>(ring + k_at[u] + 8 * e * F::kDB);
 #pragma unroll
                             for (int i = 0; i < F::kWords; i += 2) {
                                 const uint2 v = src[i / 2];
                                 w[i] = v.x;
                                 w[i + 1] = v.y;
                             }
-                            const uint32_t s2 = scale_pair(base[page * F::kDB + tok * 4 + qc] * 0x00010001u);
+                            const uint32_t s2 = scale_both(ring[ks_at[u] + 32 * e]);
                             decode<BITS>(w, s2, offset_pair<BITS>(s2), ka[e]);
                         }
 #pragma unroll
@@ -481,7 +491,8 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                                 const float mn = fmaxf(m[i][c], mx[i][c]);
                                 const float alpha = mn == -INFINITY ? 1.0f : ex2_approx(m[i][c] - mn);
                                 m[i][c] = mn;
-                                l[i][c] *= alpha;
+                                if (c == 0) l[i].x *= alpha;
+                                else l[i].y *= alpha;
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     o[i][j][c] *= alpha;
@@ -492,41 +503,36 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                     uint32_t pb[NT][2][2];
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        const float m0 = m[i][0] == -INFINITY ? 0.0f : m[i][0];
-                        const float m1 = m[i][1] == -INFINITY ? 0.0f : m[i][1];
+                        const float2 neg = make_float2(m[i][0] == -INFINITY ? 0.0f : -m[i][0],
+                                                       m[i][1] == -INFINITY ? 0.0f : -m[i][1]);
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float p0 = ex2_approx(fmaf(sc[i][u][2 * e], a.scale_log2, -m0));
-                                const float p1 = ex2_approx(fmaf(sc[i][u][2 * e + 1], a.scale_log2, -m1));
-                                l[i][0] += p0;
-                                l[i][1] += p1;
+                                const float2 x = __ffma2_rn(make_float2(sc[i][u][2 * e], sc[i][u][2 * e + 1]),
+                                                            make_float2(a.scale_log2, a.scale_log2), neg);
+                                const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                                l[i] = __fadd2_rn(l[i], p);
                                 // P enters its product rounded to bf16, as in the other attention
                                 // kernels; the sum takes it unrounded
-                                pb[i][u][e] = transpose_8x8(pack_bf16x2(p0, p1));
+                                pb[i][u][e] = transpose_8x8(pack_bf16x2(p.x, p.y));
                             }
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int kk = 32 * warp + 16 * u, slot = kk & (page - 1);
-                        const uint8_t* base = ring + (kk >> a.page_log2) * a.page_bytes;
                         uint32_t va[2][8];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int pair = slot / 2 + 4 * e + qc;
                             uint32_t w[F::kWords];
-                            const uint2* src = reinterpret_cast<const uint2*>(base + page * (F::kDB + 4) +
-                                                                              pair * (2 * F::kDB) + qg * (F::kDB / 4));
+                            const uint2* src = reinterpret_cast<const uint2*>(ring + v_at[u] + 8 * e * F::kDB);
 #pragma unroll
                             for (int i = 0; i < F::kWords; i += 2) {
                                 const uint2 v = src[i / 2];
                                 w[i] = v.x;
                                 w[i + 1] = v.y;
                             }
-                            const uint32_t sb = *reinterpret_cast<const uint16_t*>(base + page * (2 * F::kDB + 4) +
-                                                                                   pair * 8 + (qg & ~1));
-                            const uint32_t s2 = scale_pair((sb & 0xFFu) | (sb & 0xFF00u) << 8);
+                            const uint32_t s2 =
+                                scale_halves(*reinterpret_cast<const uint16_t*>(ring + vs_at[u] + 32 * e));
                             decode<BITS>(w, s2, offset_pair<BITS>(s2), va[e]);
                         }
 #pragma unroll
@@ -547,8 +553,9 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    float sum = c == 0 ? l[i].x : l[i].y;
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) l[i][c] += __shfl_xor_sync(0xffffffffu, l[i][c], d);
+                    for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     const int x = 8 * i + 2 * qc + c;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -556,7 +563,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                             make_float2(o[i][j][c], o[i][j][2 + c]);
                     if (qg == 0) {
                         ml[x] = m[i][c];
-                        ml[L::kRows + x] = l[i][c];
+                        ml[L::kRows + x] = sum;
                     }
                 }
             ok = all_agree(1, 32 * L::kWarps, ok);  // a wait that ran out ends all four warps here

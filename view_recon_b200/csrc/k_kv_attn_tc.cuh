@@ -100,7 +100,7 @@ struct KeyRegs {  // one key's K
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t out[8];
-            const uint32_t s2 = scale_pair(((scales >> (8 * c)) & 0xFFu) * 0x00010001u);
+            const uint32_t s2 = scale_both((scales >> (8 * c)) & 0xFFu);
             decode<BITS>(w[c], s2, offset_pair<BITS>(s2), out);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -145,7 +145,7 @@ struct ValueRegs {  // channels 8 ch8 .. + 7 of keys 8 oct .. + 7
         uint32_t s2[4], c2[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s2[i] = scale_pair((scales[i] & 0xFFu) | (scales[i] & 0xFF00u) << 8);
+            s2[i] = scale_halves(scales[i]);
             c2[i] = offset_pair<BITS>(s2[i]);
         }
         // V^T is two 64-key halves of 8 KB; row = channel, 16-byte chunk = key octet

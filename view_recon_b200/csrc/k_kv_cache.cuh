@@ -62,6 +62,9 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
 
 // bf16x2 scales of two scale bytes in bits 0-7 (low half) and 16-23 (high half).
 __device__ __forceinline__ uint32_t scale_pair(uint32_t bytes) { return (bytes << 4) + kScaleBf16Pair; }
+// One scale byte for both halves (a multiply-add), and two bytes of bits 0-15 for the halves.
+__device__ __forceinline__ uint32_t scale_both(uint32_t b) { return b * 0x00100010u + kScaleBf16Pair; }
+__device__ __forceinline__ uint32_t scale_halves(uint32_t b01) { return scale_pair(__byte_perm(b01, 0, 0x4140)); }
 
 // The offset that goes with a scale pair: a code enters the product as 128 + (code + 8) (4 bits)
 // or +-(128 + magnitude) (8 bits), the bf16 numbers whose low mantissa bits are the stored ones;
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheArgs a) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t out[8];
-                const uint32_t s2 = scale_pair(sb[e] * 0x00010001u);
+                const uint32_t s2 = scale_both(sb[e]);
                 decode<BITS>(w[e], s2, offset_pair<BITS>(s2), out);
                 if (live[e]) store16<T>(static_cast<T*>(a.k) + row + 64 * e, a.wide, out);
             }
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(256) read_kernel(const CacheArgs a) {
                 w[(i + 2) / F::kWords][(i + 3) % F::kWords] = q.w;
             }
             const uint32_t sb = __ldg(reinterpret_cast<const uint16_t*>(vs));
-            const uint32_t s2 = scale_pair((sb & 0xFFu) | (sb & 0xFF00u) << 8), c2 = offset_pair<BITS>(s2);
+            const uint32_t s2 = scale_halves(sb), c2 = offset_pair<BITS>(s2);
             uint32_t even[8], odd[8];  // channel pairs of each token
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
