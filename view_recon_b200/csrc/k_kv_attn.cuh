@@ -23,7 +23,7 @@ struct AttnArgs {
     float* lse;            // or null
     float* part_o;         // [2 * ctas][tile_rows][64]
     float* part_ml;        // [2 * ctas][2][tile_rows]: running max (base 2), sum
-    int4* part_rec;        // [ctas][2]: the problem that begins in a CTA's run and goes on in later ones
+    int4* part_rec;        // [ctas][2]: notes of the problems that several CTAs share
     int32_t scenes, kv_heads, group, rows;
     int32_t tile_rows, row_tiles;  // query rows per problem, problems per (scene, head)
     int32_t page_log2, n_pages, max_pages, frame;
@@ -46,6 +46,9 @@ __device__ __forceinline__ int32_t key_limit(const AttnArgs& a, const Scene& sc,
     if (pos < 0) return 0;
     return (int32_t)min(((int64_t)(pos / a.frame) + 1) * a.frame, (int64_t)sc.len);
 }
+// x / y where y is mostly 1: an integer division is a hundred dependent cycles, and the start of every
+// block would make a handful of them.
+__device__ __forceinline__ int32_t over(int32_t x, int32_t y) { return y == 1 ? x : x / y; }
 // A problem's rows are numbered row-major, the query heads of one key head innermost: row x of the
 // (scene, key head) is query row x / group of query head x % group.  Limits ascend with x.
 __device__ __forceinline__ int32_t valid_rows(const AttnArgs& a, const Scene& sc, int32_t rt) {
@@ -54,11 +57,12 @@ __device__ __forceinline__ int32_t valid_rows(const AttnArgs& a, const Scene& sc
 __device__ __forceinline__ int32_t key_tiles(const AttnArgs& a, const Scene& sc, int32_t rt) {
     const int32_t nv = valid_rows(a, sc, rt);
     if (nv == 0) return 0;
-    return (key_limit(a, sc, (rt * a.tile_rows + nv - 1) / a.group) + 127) / 128;
+    if (a.frame == 0) return (sc.len + 127) / 128;
+    return (key_limit(a, sc, over(rt * a.tile_rows + nv - 1, a.group)) + 127) / 128;
 }
 // (rows * group, scenes * row_tiles and the rows of all heads are below 2^31: checked on the host)
 __device__ __forceinline__ int64_t out_row(const AttnArgs& a, int s, int h, int32_t x) {
-    const int32_t r = x / a.group;
+    const int32_t r = over(x, a.group);
     return (int64_t)((s * a.kv_heads + h) * a.group + (x - r * a.group)) * a.rows + r;
 }
 
@@ -109,10 +113,13 @@ __device__ __forceinline__ int64_t warp_sum(int64_t x) {
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-__device__ __forceinline__ int64_t entry_cost(const AttnArgs& a, int32_t e) {
-    const int s = e / a.row_tiles, rt = e - s * a.row_tiles;
+// Cost of an entry; `empty`: it has rows, but no key for any of them.
+__device__ __forceinline__ int64_t entry_cost(const AttnArgs& a, int32_t e, bool* empty) {
+    const int s = over(e, a.row_tiles), rt = e - s * a.row_tiles;
     const Scene sc = scene_of(a, s);
-    return (int64_t)key_tiles(a, sc, rt) * tile_cost(a, valid_rows(a, sc, rt)) * a.kv_heads;
+    const int32_t nv = valid_rows(a, sc, rt), tiles = key_tiles(a, sc, rt);
+    *empty = nv > 0 && tiles == 0;
+    return (int64_t)tiles * tile_cost(a, nv) * a.kv_heads;
 }
 __device__ __forceinline__ int64_t warp_scan(int64_t c) {
     const int lane = threadIdx.x & 31;
@@ -127,9 +134,27 @@ __device__ __forceinline__ int64_t warp_scan(int64_t c) {
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
     return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
+// Rows of the problems that have no keys at all: O = 0, LSE = -inf.  Every thread of every block.
+__device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
+    const int32_t n = a.scenes * a.row_tiles;
+    for (int32_t e = blockIdx.x; e < n; e += a.ctas) {
+        const int s = over(e, a.row_tiles), rt = e - s * a.row_tiles;
+        const Scene sc = scene_of(a, s);
+        const int32_t nv = valid_rows(a, sc, rt);
+        if (nv == 0 || key_tiles(a, sc, rt) > 0) continue;
+        for (int32_t i = threadIdx.x; i < nv * a.kv_heads * 8; i += blockDim.x) {
+            const int32_t x = i / 8 % nv, h = i / 8 / nv;
+            const int64_t row = out_row(a, s, h, rt * a.tile_rows + x);
+            reinterpret_cast<uint4*>(a.o + row * 64)[i % 8] = make_uint4(0, 0, 0, 0);
+            if (a.lse && i % 8 == 0) a.lse[row] = -INFINITY;
+        }
+    }
+}
+
 // The CTA's run: cuts the list, and finds the entry in which the run begins and the place within it
 // (entry < 0: nothing to do).  Every thread of the block calls it; every warp comes to the same.  Up to
-// 32 entries are one scan in registers; for more, `red` is shared memory of one int64 per warp.
+// 32 entries are one scan in registers; for more, `red` is shared memory of one int64 per warp.  Writes
+// the rows that see no key on the way.
 struct Start {
     Cut cut;
     int64_t left, within;
@@ -141,11 +166,15 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
     Start s;
     int64_t scan = 0;
     if (n <= 32) {
-        scan = warp_scan(lane < n ? entry_cost(a, lane) : 0);
+        bool empty = false;
+        scan = warp_scan(lane < n ? entry_cost(a, lane, &empty) : 0);
         s.cut.total = __shfl_sync(0xffffffffu, scan, 31);
+        if (__any_sync(0xffffffffu, empty)) write_empty_rows(a);
     } else {
         int64_t sum = 0;
-        for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e);
+        bool empty;
+        for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e, &empty);
+        write_empty_rows(a);
         sum = warp_sum(sum);
         if (lane == 0) red[threadIdx.x >> 5] = sum;
         __syncthreads();
@@ -160,7 +189,8 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
     if (s.left <= 0) return s;
     int64_t before = 0;
     for (int32_t e0 = 0; e0 < n; e0 += 32) {
-        if (n > 32) scan = warp_scan(e0 + lane < n ? entry_cost(a, e0 + lane) : 0);
+        bool empty;
+        if (n > 32) scan = warp_scan(e0 + lane < n ? entry_cost(a, e0 + lane, &empty) : 0);
         const uint32_t past = __ballot_sync(0xffffffffu, before + scan > x);
         if (past) {
             const int first = __ffs(past) - 1;
@@ -172,23 +202,6 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
         before += __shfl_sync(0xffffffffu, scan, 31);
     }
     return s;
-}
-
-// Rows of the problems that have no keys at all: O = 0, LSE = -inf.  Every thread of every block.
-__device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
-    const int32_t n = a.scenes * a.row_tiles;
-    for (int32_t e = blockIdx.x; e < n; e += a.ctas) {
-        const int s = e / a.row_tiles, rt = e - s * a.row_tiles;
-        const Scene sc = scene_of(a, s);
-        const int32_t nv = valid_rows(a, sc, rt);
-        if (nv == 0 || key_tiles(a, sc, rt) > 0) continue;
-        for (int32_t i = threadIdx.x; i < nv * a.kv_heads * 8; i += blockDim.x) {
-            const int32_t x = i / 8 % nv, h = i / 8 / nv;
-            const int64_t row = out_row(a, s, h, rt * a.tile_rows + x);
-            reinterpret_cast<uint4*>(a.o + row * 64)[i % 8] = make_uint4(0, 0, 0, 0);
-            if (a.lse && i % 8 == 0) a.lse[row] = -INFINITY;
-        }
-    }
 }
 
 // One problem's share of a CTA's run of key tiles.
@@ -203,14 +216,25 @@ struct Segment {
     // and one of a problem that goes on after it.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1); }
 };
-// Leaves the merge kernel a note of the problem that begins in this CTA and goes on (or of none); the
+// Leaves the merge kernel notes of the problems that begin in this CTA's run and go on after it.  With
+// no more problems than CTAs a note belongs to a problem, which leaves the merge few blocks, and says
+// "none" for a problem that needs no merge; otherwise it belongs to a CTA, which has one at most.  The
 // same thread calls it before its first segment (null) and at each.
+__device__ __forceinline__ bool notes_by_problem(const AttnArgs& a) {
+    return (int64_t)a.scenes * a.row_tiles * a.kv_heads <= a.ctas;
+}
 __device__ __forceinline__ void note_parts(const AttnArgs& a, const Segment* g) {
-    int4* rec = a.part_rec + 2 * blockIdx.x;
-    if (!g)
-        rec[0] = make_int4(-1, 0, 0, 0);
-    else if (g->last >= 0) {
-        rec[1] = make_int4(g->h, g->nv, 0, 0);
+    const bool by_problem = notes_by_problem(a);
+    if (!g) {
+        bool none = !by_problem;
+        if (by_problem && (int)blockIdx.x < a.scenes * a.row_tiles * a.kv_heads) {
+            const int32_t e = over(blockIdx.x, a.kv_heads), s = over(e, a.row_tiles);
+            none = key_tiles(a, scene_of(a, s), e - s * a.row_tiles) == 0;
+        }
+        if (none) a.part_rec[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    } else if (by_problem ? g->t0 == 0 : g->last >= 0) {
+        int4* rec = a.part_rec + 2 * (by_problem ? (g->s * a.row_tiles + g->rt) * a.kv_heads + g->h : (int)blockIdx.x);
+        rec[1] = make_int4(g->h, g->nv, blockIdx.x, 0);
         rec[0] = make_int4(g->last, g->s, g->rt, 0);
     }
 }
@@ -221,16 +245,16 @@ struct Walk {
     int32_t e, h;
     __device__ __forceinline__ Walk(const AttnArgs& a, const Start& s) : left(s.left), u(0), e(s.entry), h(0) {
         if (e < 0) return;
-        const int sc = e / a.row_tiles, rt = e - sc * a.row_tiles;
+        const int sc = over(e, a.row_tiles), rt = e - sc * a.row_tiles;
         const Scene scene = scene_of(a, sc);
         const int64_t one = (int64_t)key_tiles(a, scene, rt) * tile_cost(a, valid_rows(a, scene, rt));
-        h = (int32_t)quotient(s.within, one);
+        h = s.within < one ? 0 : (int32_t)quotient(s.within, one);
         u = s.within - h * one;
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, const Cut& cut, Segment* g) {
         const int32_t n = a.scenes * a.row_tiles;
         while (left > 0 && e < n) {
-            g->s = e / a.row_tiles;
+            g->s = over(e, a.row_tiles);
             g->rt = e - g->s * a.row_tiles;
             g->sc = scene_of(a, g->s);
             g->nv = valid_rows(a, g->sc, g->rt);
@@ -321,7 +345,6 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         fence_barrier_init();
     }
     if (threadIdx.x == 0) note_parts(a, nullptr);
-    write_empty_rows(a);
     const Start start = find_start(a, red);
     const Cut cut = start.cut;
     Walk walk(a, start);
@@ -401,7 +424,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int32_t x = 8 * i + 2 * qc + j;
-                    lim[i][j] = x < nv ? key_limit(a, g.sc, (r0 + x) / a.group) : 0x7FFFFFFF;
+                    lim[i][j] = x < nv ? key_limit(a, g.sc, over(r0 + x, a.group)) : 0x7FFFFFFF;
                     least = min(least, lim[i][j]);
                 }
             }
@@ -614,85 +637,86 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 
 // ------------------------------------------------------------------------------ joining the parts
 //
-// One block per CTA of the attention kernel and 32 rows (or the whole tile of rows): the problem that
-// begins in that CTA's run and ends in another's.  A thread sums four channels of a row over the parts,
+// One block per note and 32 rows (or the whole tile of rows): a problem that begins in one CTA's run and
+// ends in another's.  A thread sums four channels of a row over the parts,
 // in order; for short tiles of rows groups of threads take every second or fourth part, and the groups
 // are summed in order.
 constexpr int kMergeThreads = 512;
 
-__global__ void __launch_bounds__(kMergeThreads) kv_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kMergeThreads, 2) kv_merge_kernel(const AttnArgs a) {
     __shared__ float4 acc_smem[32][16];
     __shared__ float ml_smem[2][32];
     wait_previous_kernel();
     const int4 r0 = __ldcg(a.part_rec + 2 * blockIdx.x), r1 = __ldcg(a.part_rec + 2 * blockIdx.x + 1);
-    const int32_t c0 = blockIdx.x, c1 = r0.x;
+    const int32_t c0 = r1.z, c1 = r0.x;
     if (c1 < 0) return;
     const int32_t nv = r1.y, rows = min(a.tile_rows, 32), groups = 32 / rows;
-    const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows, x = rows * blockIdx.y + y % rows;
-    if (rows * (int)blockIdx.y >= nv) return;
-    float m = -INFINITY, l = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (x < nv) {
-        constexpr int kBatch = 6;  // parts whose loads are in flight together: the kernel is all latency
-        for (int c = c0 + grp; c <= c1; c += groups * kBatch) {
-            float pm[kBatch], pl[kBatch];
-            float4 v[kBatch];
+    const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows;
+    for (int x = rows * blockIdx.y + y % rows; x - y % rows < nv; x += rows * gridDim.y) {
+        float m = -INFINITY, l = 0.0f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < nv) {
+            constexpr int kBatch = 6;  // parts whose loads are in flight together: the kernel is all latency
+            for (int c = c0 + grp; c <= c1; c += groups * kBatch) {
+                float pm[kBatch], pl[kBatch];
+                float4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int ci = c + i * groups;
-                pm[i] = -INFINITY;
-                pl[i] = 0.0f;
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (ci > c1) continue;
-                const int64_t slot = 2 * (int64_t)ci + (ci == c0 ? 1 : 0);
-                pm[i] = __ldcg(a.part_ml + slot * 2 * a.tile_rows + x);
-                pl[i] = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + x);
-                v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + x) * 64 + 4 * c4));
+                for (int i = 0; i < kBatch; ++i) {
+                    const int ci = c + i * groups;
+                    pm[i] = -INFINITY;
+                    pl[i] = 0.0f;
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (ci > c1) continue;
+                    const int64_t slot = 2 * (int64_t)ci + (ci == c0 ? 1 : 0);
+                    pm[i] = __ldcg(a.part_ml + slot * 2 * a.tile_rows + x);
+                    pl[i] = __ldcg(a.part_ml + (slot * 2 + 1) * a.tile_rows + x);
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot * a.tile_rows + x) * 64 + 4 * c4));
+                }
+                float mn = m;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pm[i]);
+                const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2_approx(m - mu);
+                acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float w = ex2_approx(pm[i] - mu);
+                    acc.x += v[i].x * w;
+                    acc.y += v[i].y * w;
+                    acc.z += v[i].z * w;
+                    acc.w += v[i].w * w;
+                    l += pl[i] * w;
+                }
+                m = mn;
             }
-            float mn = m;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, pm[i]);
-            const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2_approx(m - mu);
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float w = ex2_approx(pm[i] - mu);
-                acc.x += v[i].x * w;
-                acc.y += v[i].y * w;
-                acc.z += v[i].z * w;
-                acc.w += v[i].w * w;
-                l += pl[i] * w;
-            }
-            m = mn;
         }
-    }
-    if (groups > 1) {
-        acc_smem[y][c4] = acc;
-        if (c4 == 0) ml_smem[0][y] = m, ml_smem[1][y] = l;
-        __syncthreads();
-        if (grp != 0) return;
-        for (int i = 1; i < groups; ++i) m = fmaxf(m, ml_smem[0][i * rows + y]);
+        if (groups > 1) {
+            acc_smem[y][c4] = acc;
+            if (c4 == 0) ml_smem[0][y] = m, ml_smem[1][y] = l;
+            __syncthreads();
+            if (grp != 0) return;  // (shorter tiles are one round)
+            for (int i = 1; i < groups; ++i) m = fmaxf(m, ml_smem[0][i * rows + y]);
+            const float mu = m == -INFINITY ? 0.0f : m;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.0f;
+            for (int i = 0; i < groups; ++i) {
+                const float w = ex2_approx(ml_smem[0][i * rows + y] - mu);
+                const float4 v = acc_smem[i * rows + y][c4];
+                acc.x += v.x * w;
+                acc.y += v.y * w;
+                acc.z += v.z * w;
+                acc.w += v.w * w;
+                l += ml_smem[1][i * rows + y] * w;
+            }
+        }
+        if (x >= nv) continue;
         const float mu = m == -INFINITY ? 0.0f : m;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        l = 0.0f;
-        for (int i = 0; i < groups; ++i) {
-            const float w = ex2_approx(ml_smem[0][i * rows + y] - mu);
-            const float4 v = acc_smem[i * rows + y][c4];
-            acc.x += v.x * w;
-            acc.y += v.y * w;
-            acc.z += v.z * w;
-            acc.w += v.w * w;
-            l += ml_smem[1][i * rows + y] * w;
-        }
+        const int64_t row = out_row(a, r0.y, r1.x, r0.z * a.tile_rows + x);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (a.lse && c4 == 0) a.lse[row] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994530942f;
     }
-    if (x >= nv) return;
-    const float mu = m == -INFINITY ? 0.0f : m;
-    const int64_t row = out_row(a, r0.y, r1.x, r0.z * a.tile_rows + x);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    *reinterpret_cast<uint2*>(a.o + row * 64 + 4 * c4) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && c4 == 0) a.lse[row] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace kv

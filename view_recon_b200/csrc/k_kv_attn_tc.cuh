@@ -54,18 +54,15 @@ struct PageRun {
         head = a.pool + g.h * a.page_bytes;
         lim = (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len);
     }
-    // The page of token `key`, or null: past the limit, or a bad page.
-    __device__ __forceinline__ const uint8_t* of(const AttnArgs& a, int32_t key, bool* bad) const {
-        *bad = false;
-        if (key >= lim) return nullptr;
-        const uint32_t pid = (uint32_t)__ldg(row + (key >> a.page_log2));
-        if (pid >= (uint32_t)a.n_pages) {
-            *bad = true;
-            return nullptr;
-        }
-        return head + (int64_t)pid * a.page_stride;
+    // The table's entry for token `key` (-1 past the limit); nothing here waits for it.
+    __device__ __forceinline__ int32_t entry(const AttnArgs& a, int32_t key) const {
+        return key < lim ? __ldg(row + (key >> a.page_log2)) : -1;
     }
 };
+// The page that an entry names, of the problem's head, or null.
+__device__ __forceinline__ const uint8_t* page_at(const AttnArgs& a, const uint8_t* head, int32_t entry) {
+    return (uint32_t)entry < (uint32_t)a.n_pages ? head + (int64_t)entry * a.page_stride : nullptr;
+}
 
 __device__ __forceinline__ uint2 ld_shared_v2(const void* p) {
     uint2 v;
@@ -203,24 +200,24 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         *abort_flag = 0;
         fence_barrier_init();
     }
-    // thread 256 is the one that notes this block's parts
-    if (threadIdx.x == 256) note_parts(a, nullptr);
-    write_empty_rows(a);
-    const Start start = find_start(a, red);
-    const Cut cut = start.cut;
-    if (start.entry < 0) {  // the whole block: nothing to do
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        return;
-    }
-    if (warp == 0) {
+    if (warp == 1) {
         tmem_alloc(tmem_base_smem, L::kTmemCols);
         tmem_relinquish();
     }
+    // thread 256 is the one that notes this block's parts
+    if (threadIdx.x == 256) note_parts(a, nullptr);
+    const Start start = find_start(a, red);
+    const Cut cut = start.cut;
     Walk walk(a, start);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
+    if (start.entry < 0) {  // the whole block: nothing to do
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
+        return;
+    }
 
     if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------------ decode
@@ -236,22 +233,27 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
             int32_t t = g.t0, t1 = g.t1;
             KeyRegs<BITS> kr;
             ValueRegs<BITS> vr;
-            bool bad_now, bad_next, unused;
-            const uint8_t* pk = run.of(a, t * 128 + tid, &bad_now);
-            const uint8_t* pv = run.of(a, t * 128 + 8 * ValueRegs<BITS>::oct(tid), &unused);
-            kr.load(a, pk, tid);
-            vr.load(a, pv, tid);
+            int32_t ek, ev;
+            bool seen;
+            const uint8_t* head = run.head;
+            auto look_up = [&]() {
+                seen = t * 128 + tid < run.lim;
+                ek = run.entry(a, t * 128 + tid);
+                ev = run.entry(a, t * 128 + 8 * ValueRegs<BITS>::oct(tid));
+                head = run.head;
+            };
             auto advance = [&]() {
                 if (++t == t1 && (more = walk.next(a, cut, &g))) {
                     run = PageRun(a, g);
                     t = g.t0;
                     t1 = g.t1;
                 }
-                if (more) {
-                    pk = run.of(a, t * 128 + tid, &bad_next);
-                    pv = run.of(a, t * 128 + 8 * ValueRegs<BITS>::oct(tid), &unused);
-                }
+                if (more) look_up();
             };
+            look_up();
+            bool bad = seen && !page_at(a, head, ek);
+            kr.load(a, page_at(a, head, ek), tid);
+            vr.load(a, page_at(a, head, ev), tid);
             advance();
             for (int it = 0;; ++it) {
                 const int st = it % L::kStages;
@@ -259,18 +261,18 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
                 uint8_t* tile = smem + L::kKV + st * 2 * L::kTile;
                 const bool last = !more;
                 kr.store(tile, tid);
-                if (!last) kr.load(a, pk, tid);
+                if (!last) kr.load(a, page_at(a, head, ek), tid);
                 vr.store(tile + L::kTile, tid);
                 if ((tid & ((1 << a.page_log2) - 1)) == 0) {
-                    bad_pages[st * 8 + (tid >> a.page_log2)] = bad_now;
-                    if (bad_now) sa_flag_error(SA_ERR_BAD_LIST);
+                    bad_pages[st * 8 + (tid >> a.page_log2)] = bad;
+                    if (bad) sa_flag_error(SA_ERR_BAD_LIST);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && !(withhold && it == 0)) mbar_arrive(&kv_full[st]);
                 if (last) break;
-                vr.load(a, pv, tid);
-                bad_now = bad_next;
+                vr.load(a, page_at(a, head, ev), tid);
+                bad = seen && !page_at(a, head, ek);
                 advance();
             }
         }
@@ -364,6 +366,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const uint32_t tS = tmem + L::colS(half) + lane_off, tP = tmem + L::colP(half) + lane_off,
                        tO = tmem + L::colO(half) + lane_off;
+        uint8_t* rows_smem = smem + L::kQ + half * L::kTile + quad * 4096;  // this warp's rows of Q, later of O
         const float mul = a.scale_log2;
         Segment g;
         int it = 0, own = 0, joins = 0, problem = 0;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
             const int in = solo ? r : 128 * half + r;  // row within the problem
             const bool valid = in < g.nv;
             const int32_t x = g.rt * a.tile_rows + in;
-            const int64_t row = valid ? out_row(a, g.s, g.h, x) : 0;
+            const int64_t row = valid ? out_row(a, g.s, g.h, x) : -1;
             // the products that read the last Q are done: their scores have been read (and a half without
             // tiles of the last problem waits until that has been noticed)
             if (problem > 0 && !wait_warp(q_seen, (problem - 1) & 1, abort_flag)) {
@@ -382,14 +385,14 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
                 break;
             }
             ++problem;
-            {
-                uint8_t* dst = smem + L::kQ + half * L::kTile + r * 128;
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + row * 64);
+            // a warp's 32 rows, four whole rows an access (a row a lane would touch 32 lines with each)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 v = valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(dst + ((j ^ (r & 7)) << 4)) = v;
-                }
+            for (int j = 0; j < 8; ++j) {
+                const int i = 4 * j + (lane >> 3);
+                const int64_t from = __shfl_sync(0xffffffffu, row, i);
+                const uint4 v = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.q + from * 64) + (lane & 7))
+                                          : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(rows_smem + i * 128 + (((lane & 7) ^ (i & 7)) << 4)) = v;
             }
             fence_proxy_async_smem();
             const int n_tiles = g.t1 - g.t0;
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            const int32_t lim = valid ? key_limit(a, g.sc, x / a.group) : g.sc.len;
+            const int32_t lim = valid ? key_limit(a, g.sc, over(x, a.group)) : g.sc.len;
             const int32_t least = __reduce_min_sync(0xffffffffu, lim);
             float m_run = -INFINITY, l_run = 0.0f;
             const int first = solo ? half : 0, step = solo ? 2 : 1, first_own = own;
@@ -548,32 +551,49 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
                 m_run = mm;
             }
             const bool whole = g.whole();
-            const int64_t part = (int64_t)g.slot() * a.tile_rows + in;
+            const int64_t part = (int64_t)g.slot() * a.tile_rows + in - lane;  // this warp's first row
             const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
+            // rows go out through the place of Q, 128 bytes a row at a time: all of O in bf16, or a part's
+            // 32 f32 columns
 #pragma unroll 1
-            for (int c = 0; c < 64; c += 16) {
-                uint32_t ov[16];
-                tmem_ld_32x32b_x16(tO + c, ov);
-                tmem_ld_wait16(ov);
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t ov[32];
+                tmem_ld_32x32b_x32(tO + c, ov);
+                tmem_ld_wait(ov);
                 if (solo) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
+                    for (int u = 0; u < 32; ++u)
                         ov[u] = __float_as_uint(__uint_as_float(ov[u]) * f0 + join[128 * (c + u)] * f1);
                 }
-                if (valid && whole) {
-                    uint32_t w[8];
+                if (whole) {
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        w[u] = pack_bf16x2(__uint_as_float(ov[2 * u]) * inv, __uint_as_float(ov[2 * u + 1]) * inv);
-                    uint4* dst = reinterpret_cast<uint4*>(a.o + row * 64 + c);
-                    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                } else if (valid) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * 64 + c);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[j] = make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
+                        for (int u = 0; u < 4; ++u)
+                            w[u] = pack_bf16x2(__uint_as_float(ov[8 * j + 2 * u]) * inv,
+                                               __uint_as_float(ov[8 * j + 2 * u + 1]) * inv);
+                        *reinterpret_cast<uint4*>(rows_smem + lane * 128 + (((c / 8 + j) ^ (lane & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (c == 0) continue;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(rows_smem + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            make_uint4(ov[4 * j], ov[4 * j + 1], ov[4 * j + 2], ov[4 * j + 3]);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = 4 * j + (lane >> 3);
+                    const int64_t to = __shfl_sync(0xffffffffu, row, i);
+                    const uint4 v = *reinterpret_cast<const uint4*>(rows_smem + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+                    if (to < 0) continue;
+                    if (whole) *(reinterpret_cast<uint4*>(a.o + to * 64) + (lane & 7)) = v;
+                    else *(reinterpret_cast<uint4*>(a.part_o + (part + i) * 64 + c) + (lane & 7)) = v;
+                }
+                __syncwarp();
             }
             if (valid) {
                 if (!whole) {
@@ -601,7 +621,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }

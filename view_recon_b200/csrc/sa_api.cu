@@ -1580,7 +1580,7 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     // the joining kernel is launched ahead of the attention kernel's end and waits for it itself
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)((a.tile_rows + 31) / 32));
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(a.ctas, problems), (unsigned)((a.tile_rows + 31) / 32));
     cfg.blockDim = dim3(kv::kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
