@@ -284,7 +284,7 @@ struct Walk {
 
 // ------------------------------------------------------------------------------ few rows
 //
-// Up to 32 query rows a problem: bound by the reading and decoding of the pages, so the rows ride on
+// Up to 32 query rows a problem (48 in two): bound by the reading and decoding of the pages, so the rows ride on
 // the narrow side of mma.sync (m16n8k16, keys on m, rows on n): S^T = K Q^T with 16 keys x 8 rows,
 // O^T += V^T P^T with 16 channels x 8 rows.  A lane's decoded words are its operand registers as they
 // stand (the page layout is made for it): no shuffle and no shared-memory round trip between a
@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv_merge_kernel(const AttnAr
     if (c1 < 0) return;
     const int32_t nv = r1.y, rows = min(a.tile_rows, 32), groups = 32 / rows;
     const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows;
+    if (grp >= groups) return;  // 24 rows leave a quarter of the threads over
     for (int x = rows * blockIdx.y + y % rows; x - y % rows < nv; x += rows * gridDim.y) {
         float m = -INFINITY, l = 0.0f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -1,4 +1,4 @@
-// Attention over the frame cache for more than 32 query rows a problem (whole frames): the
+// Attention over the frame cache for more than 48 query rows a problem (whole frames): the
 // products on the 5th-generation tensor cores, 128 keys a step, scores and O in tensor memory.
 // One block per SM, two halves: each takes 128 of a problem's 256 query rows through the same decoded
 // keys, so that a page is decoded once for both and one half's exponentials fill the other's waits.  A

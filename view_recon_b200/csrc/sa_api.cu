@@ -1361,9 +1361,16 @@ dim3 kv_rows_grid(const sa_kv_cache* c, int32_t n) {
     return dim3((unsigned)((int64_t)c->scenes * c->heads), (unsigned)std::min<int64_t>(chunks, 65535));
 }
 
-// Query rows of one problem: all rows of a key head's query heads together, in the smallest tile of
-// the few-rows kernel, or 256 at a time on the tensor cores.
-int32_t kv_tile_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kv::kPairRows; }
+// Query rows of one problem: all rows of a key head's query heads together in the smallest tile of
+// the few-rows kernel that holds them, or two of 24, or 256 at a time in the tcgen05 kernel.  Both sides
+// of the border, 16 heads in 4 bits: 48 rows over 30 011 tokens 39.6 us in two tiles of 24 and 48.5 us
+// there, 64 rows 51.6 us in two tiles of 32 and 48.8 us there (over 175 872 tokens 174 against 209 us, and
+// 231 against 210 us).
+int32_t kv_tile_rows(int64_t rows) {
+    if (rows <= 32) return (int32_t)std::max<int64_t>(8, (rows + 7) / 8 * 8);
+    if (rows <= 48) return 24;
+    return kv::kPairRows;
+}
 
 // Largest grids of the attention kernels: what the workspace has room for.
 int kv_max_ctas(int32_t tile_rows) { return tile_rows == kv::kPairRows ? 160 : 640; }
@@ -1384,7 +1391,7 @@ sa_status kv_attn_check(const sa_kv_cache* c, int32_t q_heads, int32_t rows, KvG
 }
 
 std::mutex g_kv_mu;
-int g_kv_grid[kMaxDevices][2][4];  // resident blocks of each attention kernel, per device
+int g_kv_grid[kMaxDevices][2][5];  // resident blocks of each attention kernel, per device
 
 // Launches an attention kernel with as many blocks as stay resident (each takes an equal run of
 // key tiles); `which` names the kernel's place in g_kv_grid.
@@ -1401,7 +1408,7 @@ sa_status kv_launch(void (*kernel)(const kv::AttnArgs), kv::AttnArgs& a, int dev
                 return SA_ERR_CUDA;
             }
             if (per_sm < 1) return SA_ERR_UNSUPPORTED;
-            if (which == 3) {
+            if (which == 4) {
                 // one block has all of an SM's tensor memory; its register split needs what it hands out
                 per_sm = 1;
                 cudaFuncAttributes fa;
@@ -1428,10 +1435,13 @@ sa_status kv_launch_rows(kv::AttnArgs& a, int dev, cudaStream_t stream) {
     if (a.tile_rows == 16)
         return kv_launch(kv::kv_few_rows_kernel<BITS, 2>, a, dev, BITS, 1, FewLayout<BITS, 2>::kThreads,
                          FewLayout<BITS, 2>::smem_bytes(), stream);
+    if (a.tile_rows == 24)
+        return kv_launch(kv::kv_few_rows_kernel<BITS, 3>, a, dev, BITS, 2, FewLayout<BITS, 3>::kThreads,
+                         FewLayout<BITS, 3>::smem_bytes(), stream);
     if (a.tile_rows == 32)
-        return kv_launch(kv::kv_few_rows_kernel<BITS, 4>, a, dev, BITS, 2, FewLayout<BITS, 4>::kThreads,
+        return kv_launch(kv::kv_few_rows_kernel<BITS, 4>, a, dev, BITS, 3, FewLayout<BITS, 4>::kThreads,
                          FewLayout<BITS, 4>::smem_bytes(), stream);
-    return kv_launch(kv::kv_tc_kernel<BITS>, a, dev, BITS, 3, kv::TcLayoutKv::kThreads, kv::TcLayoutKv::smem_bytes(),
+    return kv_launch(kv::kv_tc_kernel<BITS>, a, dev, BITS, 4, kv::TcLayoutKv::kThreads, kv::TcLayoutKv::smem_bytes(),
                      stream);
 }
 
