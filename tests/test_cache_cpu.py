@@ -223,11 +223,17 @@ def test_wrap_and_layer_refusals(lib):
         c.append(x, x, new_len=torch.zeros(1))
     with pytest.raises(ValueError):
         c.read()
+    with pytest.raises(ValueError, match="CUDA"):    # bookkeeping works on the host, calls do not
+        c.append(x, x)
+    with pytest.raises(ValueError, match="CUDA"):
+        c.read(x, x)
     for rows, heads in ((0, 2), (3, 3), (3, 0)):
         with pytest.raises(ValueError):
             CachedGlobalAttention(c, rows, q_heads=heads)
     layer = CachedGlobalAttention(c, 3, q_heads=4)
     assert layer.o.shape == (4, 3, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        layer.forward(torch.zeros(4, 3, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         layer.forward(torch.zeros(4, 3, 64))
     with pytest.raises(ValueError):

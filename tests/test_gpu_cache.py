@@ -289,6 +289,79 @@ def test_attention_many_short_scenes_and_long_ones(rows):
     _attend(p, rng, rows, p.heads, taken=[int(x) for x in rng.integers(0, rows + 1, len(lens))])
 
 
+@pytest.mark.parametrize("rows", [8, 16, 17, 24, 25, 32, 34, 48, 49, 64, 127, 128, 129, 255, 256, 257, 400])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_attention_every_row_tile_and_its_borders(rows, bits):
+    """Row counts on both sides of every tile and kernel border, over scenes that one block takes alone
+    and scenes that many share."""
+    rng = np.random.default_rng(rows + bits)
+    p = Pool(rng, [5000, 140, 0, rows], 1, 64, bits)
+    _fill(p, rng)
+    _attend(p, rng, rows, 1)
+    _attend(p, rng, rows, 1, frame=33, taken=[rows, rows // 2, rows, max(0, rows - 1)])
+
+
+@pytest.mark.parametrize("rows", [1, 20, 60, 300])
+def test_attention_more_problems_than_blocks_all_cut(rows):
+    """Many heads of a length that leaves nearly every block with an end and a beginning."""
+    rng = np.random.default_rng(rows)
+    p = Pool(rng, [1700], 61, 128, 8)
+    _fill(p, rng)
+    _attend(p, rng, rows, 61 * 2 if rows < 50 else 61)
+
+
+@pytest.mark.parametrize("rows", [3, 150])
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives(rows):
+    from view_recon_b200 import sa
+    import time
+    rng = np.random.default_rng(17)
+    p = Pool(rng, [2000, 7], 3, 64, 4)
+    _fill(p, rng)
+    _, tq, layer = _attend(p, rng, rows, 3)
+    layer.ws.random_(0, 256)   # notes of an earlier call would name parts that this one has not made
+    try:
+        sa.sa_set_wait_limit_ns(50_000_000)
+        sa.sa_test_withhold_query_load(True)
+        t0 = time.time()
+        layer.forward(tq)
+        status = sa.sa_check_device_error()
+        elapsed = time.time() - t0
+    finally:
+        sa.sa_test_withhold_query_load(False)
+        sa.sa_set_wait_limit_ns(2_000_000_000)
+    assert status == sa.SA_ERR_TIMEOUT and elapsed < 20.0
+    _ok()
+    _attend(p, rng, rows, 3)
+
+
+@pytest.mark.parametrize("bits,dtype", [(4, "bf16"), (8, "f32")])
+def test_rows_on_sixteen_byte_boundaries(bits, dtype):
+    """Rows that start 16 bytes past a 32-byte boundary, and the refusal of less."""
+    import torch
+    rng = np.random.default_rng(18)
+    p = Pool(rng, [77], 2, 32, bits)
+    k, tk = _rows(rng, (2, 77, 64), dtype)
+    off = 16 // tk.element_size()
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + off, dtype=t.dtype, device="cuda")
+        out = buf[off:].view(t.shape)
+        out.copy_(t)
+        assert out.data_ptr() % 32 == 16
+        return out
+
+    p.cache.append(shifted(tk), shifted(tk))
+    a, b = p.cache.read(shifted(torch.zeros_like(tk)), shifted(torch.zeros_like(tk)))
+    _ok()
+    ref = orc.cache_numbers(k, bits)
+    assert np.array_equal(H.from_device(a), ref) and np.array_equal(H.from_device(b), ref)
+    bad = torch.zeros(tk.numel() + 1, dtype=tk.dtype, device="cuda")[1:].view(tk.shape)
+    with pytest.raises(ValueError):
+        p.cache.append(bad, tk)
+    with pytest.raises(ValueError):
+        p.cache.append(tk.cpu(), tk.cpu())
+
+
 @pytest.mark.parametrize("rows", [2, 150])
 @pytest.mark.parametrize("scale", [0.02, 1.0])
 def test_attention_scales_and_peaked_rows(rows, scale):

@@ -216,28 +216,6 @@ struct Segment {
     // and one of a problem that goes on after it.
     __device__ __forceinline__ int slot() const { return 2 * (int)blockIdx.x + (t0 > 0 ? 0 : 1); }
 };
-// Leaves the merge kernel notes of the problems that begin in this CTA's run and go on after it.  With
-// no more problems than CTAs a note belongs to a problem, which leaves the merge few blocks, and says
-// "none" for a problem that needs no merge; otherwise it belongs to a CTA, which has one at most.  The
-// same thread calls it before its first segment (null) and at each.
-__device__ __forceinline__ bool notes_by_problem(const AttnArgs& a) {
-    return (int64_t)a.scenes * a.row_tiles * a.kv_heads <= a.ctas;
-}
-__device__ __forceinline__ void note_parts(const AttnArgs& a, const Segment* g) {
-    const bool by_problem = notes_by_problem(a);
-    if (!g) {
-        bool none = !by_problem;
-        if (by_problem && (int)blockIdx.x < a.scenes * a.row_tiles * a.kv_heads) {
-            const int32_t e = over(blockIdx.x, a.kv_heads), s = over(e, a.row_tiles);
-            none = key_tiles(a, scene_of(a, s), e - s * a.row_tiles) == 0;
-        }
-        if (none) a.part_rec[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-    } else if (by_problem ? g->t0 == 0 : g->last >= 0) {
-        int4* rec = a.part_rec + 2 * (by_problem ? (g->s * a.row_tiles + g->rt) * a.kv_heads + g->h : (int)blockIdx.x);
-        rec[1] = make_int4(g->h, g->nv, blockIdx.x, 0);
-        rec[0] = make_int4(g->last, g->s, g->rt, 0);
-    }
-}
 // Walks the CTA's run; every role of the CTA makes the same walk.  A tile belongs to the run in which
 // its place in the list (cost by cost) begins.
 struct Walk {
@@ -281,6 +259,31 @@ struct Walk {
         return false;
     }
 };
+
+// Leaves the merge kernel notes of the problems that begin in this CTA's run and go on after it.  With
+// no more problems than CTAs a note belongs to a problem, which leaves the merge few blocks, and says
+// "none" for a problem that needs no merge; otherwise it belongs to a CTA, which has one at most.  One
+// thread writes them all before anything can fail: whatever a wait that runs out leaves undone, the
+// merge kernel reads notes of this launch.
+__device__ __forceinline__ bool notes_by_problem(const AttnArgs& a) {
+    return (int64_t)a.scenes * a.row_tiles * a.kv_heads <= a.ctas;
+}
+__device__ __forceinline__ void note_parts(const AttnArgs& a, const Cut& cut, Walk walk) {
+    const bool by_problem = notes_by_problem(a);
+    bool none = !by_problem;
+    if (by_problem && (int)blockIdx.x < a.scenes * a.row_tiles * a.kv_heads) {
+        const int32_t e = over(blockIdx.x, a.kv_heads), s = over(e, a.row_tiles);
+        none = key_tiles(a, scene_of(a, s), e - s * a.row_tiles) == 0;
+    }
+    if (none) a.part_rec[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+    Segment g;
+    while (walk.next(a, cut, &g)) {
+        if (!(by_problem ? g.t0 == 0 : g.last >= 0)) continue;
+        int4* rec = a.part_rec + 2 * (by_problem ? (g.s * a.row_tiles + g.rt) * a.kv_heads + g.h : (int)blockIdx.x);
+        rec[1] = make_int4(g.h, g.nv, blockIdx.x, 0);
+        rec[0] = make_int4(g.last, g.s, g.rt, 0);
+    }
+}
 
 // ------------------------------------------------------------------------------ few rows
 //
@@ -344,7 +347,6 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (threadIdx.x == 0) note_parts(a, nullptr);
     const Start start = find_start(a, red);
     const Cut cut = start.cut;
     Walk walk(a, start);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     int it = 0;  // tiles so far: ring stage it % kStages
     if (warp == L::kWarps) {
         // ---------------------------------------------------------------- loads
-        bool ok = true;
+        bool ok = !(g_sa_test_withhold != 0 && blockIdx.x == 0);
         while (ok && walk.next(a, cut, &g)) {
             const int32_t* row = a.table + (int64_t)g.s * a.max_pages;
             const int32_t lim = (int32_t)min((int64_t)g.tiles * 128, (int64_t)g.sc.len);
@@ -388,6 +390,8 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     } else {
         // ---------------------------------------------------------------- products
         const int qg = lane >> 2, qc = lane & 3;
+        if (threadIdx.x == 0) note_parts(a, cut, walk);  // while the first tile is on its way
+        __syncwarp();
         // where this lane's codes and scales of its 32 keys are within a stage, 16 keys at a time (a page
         // holds 16 keys at least)
         int k_at[2], ks_at[2], v_at[2], vs_at[2];
@@ -402,7 +406,6 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         }
         bool ok = true;
         while (ok && walk.next(a, cut, &g)) {
-            if (threadIdx.x == 0) note_parts(a, &g);
             const int32_t nv = g.nv;
             const int32_t r0 = g.rt * a.tile_rows;
             // Q^T operand: row 8 i + qg, channels 16 qc .. 16 qc + 15
@@ -648,7 +651,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) kv_merge_kernel(const AttnAr
     __shared__ float ml_smem[2][32];
     wait_previous_kernel();
     const int4 r0 = __ldcg(a.part_rec + 2 * blockIdx.x), r1 = __ldcg(a.part_rec + 2 * blockIdx.x + 1);
-    const int32_t c0 = r1.z, c1 = r0.x;
+    const int32_t c0 = r1.z, c1 = min(r0.x, a.ctas - 1);
     if (c1 < 0) return;
     const int32_t nv = r1.y, rows = min(a.tile_rows, 32), groups = 32 / rows;
     const int y = threadIdx.x / 16, c4 = threadIdx.x % 16, grp = y / rows;

@@ -204,8 +204,6 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         tmem_alloc(tmem_base_smem, L::kTmemCols);
         tmem_relinquish();
     }
-    // thread 256 is the one that notes this block's parts
-    if (threadIdx.x == 256) note_parts(a, nullptr);
     const Start start = find_start(a, red);
     const Cut cut = start.cut;
     Walk walk(a, start);
@@ -213,6 +211,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
+    if (threadIdx.x == 64) note_parts(a, cut, walk);  // (of a warp without other work)
     if (start.entry < 0) {  // the whole block: nothing to do
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         int it = 0, own = 0, joins = 0, problem = 0;
         bool ok = true;
         while (ok && walk.next(a, cut, &g)) {
-            if (threadIdx.x == 256) note_parts(a, &g);
             const bool solo = is_solo(a, g.nv);
             const int in = solo ? r : 128 * half + r;  // row within the problem
             const bool valid = in < g.nv;

@@ -484,6 +484,8 @@ class FrameCache:
         """One C call on the cache's device, on `stream` or the device's current one."""
         import torch
         index = self.device.index
+        if index is None:
+            raise ValueError("the cache is not on a CUDA device")
         if torch.cuda.current_device() == index:
             st = fn(self._ref, *args, sa.raw_stream(index, stream))
         else:
