@@ -21,7 +21,7 @@ namespace kv {
 struct TcLayoutKv {
     static constexpr int kThreads = 512;
     // registers per thread after the split (launched with 128 each; the sum is the launch's own)
-    static constexpr uint32_t kRegsIssue = 48, kRegsDecode = 96, kRegsSoftmax = 184;
+    static constexpr uint32_t kRegsIssue = 40, kRegsDecode = 88, kRegsSoftmax = 192;
     static constexpr uint32_t kRegsNeeded = 128 * (kRegsIssue + kRegsDecode + 2 * kRegsSoftmax);
     static constexpr int kStages = 4;
     static constexpr int kTile = 128 * 128;  // bytes of a 128 x 64 bf16 operand
