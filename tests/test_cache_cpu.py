@@ -238,3 +238,11 @@ def test_wrap_and_layer_refusals(lib):
         layer.forward(torch.zeros(4, 3, 64))
     with pytest.raises(ValueError):
         layer.forward(torch.zeros(4, 2, 64, dtype=torch.bfloat16))
+
+
+def test_grow_takes_any_integer(lib):
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(2, 1, tokens=64, page=16, device="cpu")
+    c.grow(np.int64(3))
+    c.grow(np.array([1, 14], dtype=np.int32))
+    assert c.lens.tolist() == [4, 17]

@@ -622,3 +622,50 @@ def test_streaming_frames_as_they_would_be_used():
     # each is within 2^-8 (|O| + A) of the exact value, |O| <= A <= max |v|
     assert (o[:heads].float() - od.float()).abs().max().item() <= 4 * 2.0 ** -8 * v.abs().max().item()
     assert (lse[:heads] - ld).abs().max().item() <= 1e-3
+
+
+def test_pages_and_lengths_stay_out_of_graphs():
+    import torch
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(2, 2, tokens=200, page=16)
+    c.grow([20, 5])
+    x = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1)
+        with pytest.raises(RuntimeError):
+            c.grow(1)
+        with pytest.raises(RuntimeError):
+            c.release(0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [1.0] * 8 and c.lens.tolist() == [20, 5] and c._len == [20, 5]
+    assert (c.page_table >= 0).sum().item() == 3
+
+
+def test_growing_in_step_with_queued_work():
+    """Lengths and pages sent while earlier calls are still queued arrive in their turn: every call sees its own."""
+    import torch
+    from view_recon_b200.pipeline import CachedGlobalAttention, FrameCache
+    rng = np.random.default_rng(21)
+    N, steps, heads = 37, 24, 2
+    rows = [_rows(rng, (heads, N, 64), "bf16") for _ in range(2 * steps)]
+    q, tq = _rows(rng, (heads, 4, 64), "bf16")
+    c = FrameCache(1, heads, tokens=N * steps, page=16)
+    layer = CachedGlobalAttention(c, 4)
+    busy = torch.randn((6000, 6000), device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(8):
+        busy = busy @ busy * 1e-3                  # some milliseconds of work ahead of the first copy
+    outs = []
+    for i in range(steps):
+        c.grow(N)
+        c.append(rows[2 * i][1], rows[2 * i + 1][1])
+        outs.append(layer.forward(tq)[0].clone())
+    _ok()
+    for i in (0, 1, 7, steps - 1):
+        k = np.concatenate([orc.cache_numbers(rows[2 * j][0], 4) for j in range(i + 1)], 1)
+        v = np.concatenate([orc.cache_numbers(rows[2 * j + 1][0], 4) for j in range(i + 1)], 1)
+        ref, _, A, _ = orc.cache_attend(q, k, v, 0.125, 0)
+        assert (np.abs(H.from_device(outs[i]) - ref) <= _bar(ref, A)).all()

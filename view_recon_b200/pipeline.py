@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import numbers
 
 from . import sa
 
@@ -438,13 +439,28 @@ class FrameCache:
     def _owned(self):
         if not self._owner:
             raise ValueError("pages and lengths of this cache are managed elsewhere")
+        if self.device.type == "cuda":
+            import torch
+            with torch.cuda.device(self.device):
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("pages and lengths are the host's: change them outside a recorded graph")
+
+    def _send(self, values, dtype):
+        """Host numbers on the device.  From pinned memory, so that the host does not wait for the work that is
+        queued before the copy (torch keeps the pinned block until the copy has run)."""
+        import torch
+        pin = self.device.type == "cuda"
+        return torch.tensor(values, dtype=dtype, pin_memory=pin).to(self.device, non_blocking=pin)
+
+    def _send_lengths(self):
+        import torch
+        self.lens.copy_(self._send(self._len, torch.int32))
 
     def grow(self, n):
         """Count n more tokens (one number, or one per scene) into the cache and give them pages.  Call it once
         before the layers' appends.  Raises MemoryError, changing nothing, when pages run out."""
-        import torch
         self._owned()
-        ns = [int(n)] * self.scenes if isinstance(n, int) else [int(x) for x in n]
+        ns = [int(n)] * self.scenes if isinstance(n, numbers.Integral) else [int(x) for x in n]
         if len(ns) != self.scenes or min(ns) < 0:
             raise ValueError("grow needs one non-negative count, or one per scene")
         need = [-(-(self._len[s] + ns[s]) // self.page) for s in range(self.scenes)]
@@ -462,19 +478,19 @@ class FrameCache:
                 self._pages[s].append(ids[-1])
             self._len[s] += ns[s]
         if ids:
-            at = torch.tensor([rows, cols, ids], dtype=torch.int64).to(self.device)
+            import torch
+            at = self._send([rows, cols, ids], torch.int64)
             self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
-        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+        self._send_lengths()
 
     def release(self, scene: int):
         """Drop a scene: its pages are free again and its length is 0."""
-        import torch
         self._owned()
         self._free.extend(reversed(self._pages[scene]))
         self._pages[scene] = []
         self._len[scene] = 0
         self.page_table[scene].fill_(-1)
-        self.lens.copy_(torch.tensor(self._len, dtype=torch.int32))
+        self._send_lengths()
 
     # ---- rows (each one C call)
     def _counts(self, name, t):
@@ -532,7 +548,8 @@ class CachedGlobalAttention:
                their own and earlier frames of n tokens (1: causal by token)
 
     Workspace and outputs are allocated once: an object's calls (and graphs recorded from it) run one
-    after another; calls that overlap need an object each."""
+    after another; calls that overlap need an object each.  For inference: the outputs carry no gradient
+    (the stored numbers are rounded)."""
 
     def __init__(self, cache: FrameCache, rows: int, q_heads: int | None = None, frame: int = 0,
                  softmax_scale: float = 0.0, with_lse: bool = True):
@@ -563,11 +580,14 @@ class CachedGlobalAttention:
 
     def capture(self, q, q_len=None):
         """Record one call on these tensors as a CUDA graph.  A replay follows the cache's lengths and page
-        table as they are then (frames appended in between are seen) and new queries written into q."""
+        table as they are then (frames appended in between are seen) and new queries written into q.  Keep this
+        object, the cache, q and q_len for as long as the graph."""
         import torch
+        dev = self.cache.device
         self.forward(q, q_len)
-        torch.cuda.current_stream(self.cache.device).synchronize()
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            self.forward(q, q_len)
+        with torch.cuda.device(dev):
+            torch.cuda.current_stream(dev).synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=torch.cuda.Stream(dev)):
+                self.forward(q, q_len)
         return g
