@@ -1580,7 +1580,6 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     a.min_units = a.tile_rows == kv::kPairRows ? kv::kPairCost : 1;  // a run as long as one tile holds one's beginning
     a.page_bytes = g.page_bytes;
     a.page_stride = g.page_bytes * cache->heads;
-    a.page_stride = g.page_bytes * cache->heads;
     const float scale = softmax_scale > 0.0f ? softmax_scale : 0.125f;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     const int64_t problems = (int64_t)a.scenes * a.row_tiles * a.kv_heads;
