@@ -95,7 +95,8 @@ __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepco
 
 // The tensor-core kernel takes 256 rows a problem, 128 in each half of a block.  One that has at most
 // 128 of them is done by both halves together, every other key tile each ("solo").  Cost of a key tile:
-// about its time (a solo tile has half the work, but the whole decoding).
+// about its time (a solo tile has half the products and exponentials, but the whole decoding): 2.0 us of
+// an SM against 1.5 in 4 bits, 2.1 against 1.8 in 8 bits (16 heads, 87 936 tokens, 256 and 128 rows).
 constexpr int kPairRows = 256;
 constexpr int kPairCost = 4, kSoloCost = 3;
 __device__ __forceinline__ bool is_solo(const AttnArgs& a, int32_t nv) { return a.tile_rows == kPairRows && nv <= 128; }
@@ -287,13 +288,21 @@ __device__ __forceinline__ void note_parts(const AttnArgs& a, const Cut& cut, Wa
 
 // ------------------------------------------------------------------------------ few rows
 //
-// Up to 32 query rows a problem (48 in two): bound by the reading and decoding of the pages, so the rows ride on
-// the narrow side of mma.sync (m16n8k16, keys on m, rows on n): S^T = K Q^T with 16 keys x 8 rows,
-// O^T += V^T P^T with 16 channels x 8 rows.  A lane's decoded words are its operand registers as they
-// stand (the page layout is made for it): no shuffle and no shared-memory round trip between a
-// page's bytes and the tensor cores; P^T is transposed by one movmatrix per 8 x 8.
+// Up to 32 query rows a problem (48 in two): every page is read and decoded for few products, so the
+// rows ride on the narrow side of mma.sync (m16n8k16, keys on m, rows on n): S^T = K Q^T with 16 keys x
+// 8 rows, O^T += V^T P^T with 16 channels x 8 rows (tcgen05 would take 128 rows, mostly padding, and
+// operands through shared memory).  A lane's decoded words are its operand registers as they stand (the
+// page layout is made for it): no shuffle and no shared-memory round trip between a page's bytes and
+// the tensor cores; P^T is transposed by one movmatrix per 8 x 8.
 // Four warps take 32 keys each of every 128-key tile; a fifth keeps a ring of tiles in flight with
 // bulk copies of whole pages (K, V and scales of a page and head are one run of bytes).
+// Measured, 16 heads: 5 rows over 351 744 tokens in 4 bits 103 us, 3.9 TB/s, bound by instruction issue
+// (65 % of the slots, the ALU pipe 57 %; 1483 warp instructions a tile; the same ring with nothing done
+// to the tiles takes 73 us, everything but the decoding 76 us).  In 8 bits, with more bytes to the
+// instruction, 5.8 TB/s; with 12 rows 5.0 TB/s.
+// Blocks an SM, by groups of 8 rows: 4, 3, 2, 2 (what the registers allow without spills).  One group
+// with 5 blocks and 3 stages: 111 us against 104; two groups with 4: 174 against 133; four groups
+// with 3: 324 against 241.
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -641,9 +650,11 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
 // ------------------------------------------------------------------------------ joining the parts
 //
 // One block per note and 32 rows (or the whole tile of rows): a problem that begins in one CTA's run and
-// ends in another's.  A thread sums four channels of a row over the parts,
-// in order; for short tiles of rows groups of threads take every second or fourth part, and the groups
-// are summed in order.
+// ends in another's.  O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its parts i.  A thread sums
+// four channels of a row over the parts, in order; for short tiles of rows groups of threads take every
+// second or fourth part, and the groups are summed in order.  A chain of a few loads, not bandwidth, is
+// its time: launched early, with six parts in flight and no block for a problem without parts, a call of
+// 1 row over 2 748 tokens and 16 heads came down from 12.4 to 9.4 us in a recorded graph.
 constexpr int kMergeThreads = 512;
 
 __global__ void __launch_bounds__(kMergeThreads, 2) kv_merge_kernel(const AttnArgs a) {

@@ -1372,7 +1372,8 @@ int32_t kv_tile_rows(int64_t rows) {
     return kv::kPairRows;
 }
 
-// Largest grids of the attention kernels: what the workspace has room for.
+// Largest grids of the attention kernels, which the workspace has room for: one block, or four, on each of
+// 160 SMs (the workspace's size must not depend on the device that asks).
 int kv_max_ctas(int32_t tile_rows) { return tile_rows == kv::kPairRows ? 160 : 640; }
 
 size_t kv_part_bytes(int32_t tile_rows) {

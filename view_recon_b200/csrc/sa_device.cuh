@@ -16,7 +16,8 @@ __device__ int g_sa_error = 0;
 // Upper bound on any single device-side wait, in globaltimer nanoseconds.
 __device__ unsigned long long g_sa_wait_limit_ns = 2000000000ull;
 // Test facility (sa_test_withhold_query_load): when nonzero, CTA 0 of the tensor-core attention
-// kernel never issues its first query-tile load, so one wait can only end by running out.
+// kernel never issues its first query-tile load (in attention over the frame cache: never hands over
+// its first key tile), so one wait can only end by running out.
 __device__ int g_sa_test_withhold = 0;
 
 __device__ __forceinline__ void sa_flag_error(int code) { atomicCAS(&g_sa_error, 0, code); }
