@@ -669,3 +669,20 @@ def test_growing_in_step_with_queued_work():
         v = np.concatenate([orc.cache_numbers(rows[2 * j + 1][0], 4) for j in range(i + 1)], 1)
         ref, _, A, _ = orc.cache_attend(q, k, v, 0.125, 0)
         assert (np.abs(H.from_device(outs[i]) - ref) <= _bar(ref, A)).all()
+
+
+@pytest.mark.parametrize("scenes", [14, 66])
+@pytest.mark.parametrize("rows,bits", [(2, 8), (20, 4), (100, 8), (300, 4)])
+def test_attention_long_runs_of_problems(rows, bits, scenes):
+    """So much work that a problem's beginning counts in the cut; short problems beside long ones."""
+    rng = np.random.default_rng(rows + scenes)
+    heads = 14 if scenes == 14 else 4
+    lens = [1900 + int(x) for x in rng.integers(0, 200, scenes)]
+    lens[3:6] = [0, 1, 130]
+    p = Pool(rng, lens, heads, 128, bits)
+    _fill(p, rng)
+    taken = [rows] * scenes
+    taken[1], taken[6] = 0, max(1, rows // 3)
+    _attend(p, rng, rows, heads, taken=taken)
+    if rows in (20, 300):
+        _attend(p, rng, rows, heads, frame=7, taken=taken)

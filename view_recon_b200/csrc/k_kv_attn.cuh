@@ -27,7 +27,8 @@ struct AttnArgs {
     int32_t scenes, kv_heads, group, rows;
     int32_t tile_rows, row_tiles;  // query rows per problem, problems per (scene, head)
     int32_t page_log2, n_pages, max_pages, frame;
-    int32_t ctas, min_units;  // grid of the attention kernel, least cost of a CTA's run
+    int32_t ctas;             // grid of the attention kernel
+    int32_t tile_cost, solo_cost, start_cost;  // of a key tile and of beginning a problem (kv_costs)
     int64_t page_bytes, page_stride;  // of one page of one head, of a page of every head
     float scale_log2;
 };
@@ -94,27 +95,24 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The tensor-core kernel takes 256 rows a problem, 128 in each half of a block.  One that has at most
-// 128 of them is done by both halves together, every other key tile each ("solo").  Cost of a key tile:
-// about its time (a solo tile has half the products and exponentials, but the whole decoding): 2.0 us of
-// an SM against 1.5 in 4 bits, 2.1 against 1.8 in 8 bits (16 heads, 87 936 tokens, 256 and 128 rows).
+// 128 of them is done by both halves together, every other key tile each ("solo").
 constexpr int kPairRows = 256;
-constexpr int kPairCost = 4, kSoloCost = 3;
 __device__ __forceinline__ bool is_solo(const AttnArgs& a, int32_t nv) { return a.tile_rows == kPairRows && nv <= 128; }
 __device__ __forceinline__ int32_t tile_cost(const AttnArgs& a, int32_t nv) {
-    return a.tile_rows != kPairRows ? 1 : nv > 128 ? kPairCost : kSoloCost;
+    return is_solo(a, nv) ? a.solo_cost : a.tile_cost;
 }
 
 // The list of problems, entry e = (scene e / row_tiles, row tile e % row_tiles), heads within.
 struct Cut {
-    int64_t total;  // cost of all key tiles
-    int64_t per;    // of one CTA's run
+    int64_t per;    // cost of one CTA's run
+    int32_t start;  // of beginning a problem: its first tile costs this much more
 };
 __device__ __forceinline__ int64_t warp_sum(int64_t x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
-// Cost of an entry; `empty`: it has rows, but no key for any of them.
+// Cost of an entry's key tiles; `empty`: it has rows, but no key for any of them.
 __device__ __forceinline__ int64_t entry_cost(const AttnArgs& a, int32_t e, bool* empty) {
     const int s = over(e, a.row_tiles), rt = e - s * a.row_tiles;
     const Scene sc = scene_of(a, s);
@@ -152,46 +150,63 @@ __device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
     }
 }
 
-// The CTA's run: cuts the list, and finds the entry in which the run begins and the place within it
-// (entry < 0: nothing to do).  Every thread of the block calls it; every warp comes to the same.  Up to
-// 32 entries are one scan in registers; for more, `red` is shared memory of one int64 per warp.  Writes
-// the rows that see no key on the way.
+// The CTA's run: the cut of the list, and the entry in which the run begins and the place within it
+// (entry < 0: nothing to do).
 struct Start {
     Cut cut;
     int64_t left, within;
-    int32_t entry;
+    int32_t entry, any_empty;  // any_empty: rows without keys have to be written
 };
+// Up to 32 entries are one scan in the registers of the warp that calls this; for more every thread of the
+// block calls it, and `red` is shared memory of two int64 per warp.
 __device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
     const int lane = threadIdx.x & 31;
     const int32_t n = a.scenes * a.row_tiles;
     Start s;
-    int64_t scan = 0;
+    int64_t scan = 0, cost = 0, total = 0;
+    int32_t busy = 0;  // entries with key tiles
     if (n <= 32) {
         bool empty = false;
-        scan = warp_scan(lane < n ? entry_cost(a, lane, &empty) : 0);
-        s.cut.total = __shfl_sync(0xffffffffu, scan, 31);
-        if (__any_sync(0xffffffffu, empty)) write_empty_rows(a);
+        cost = lane < n ? entry_cost(a, lane, &empty) : 0;
+        scan = warp_scan(cost);
+        total = __shfl_sync(0xffffffffu, scan, 31);
+        busy = __popc(__ballot_sync(0xffffffffu, cost > 0));
+        s.any_empty = __any_sync(0xffffffffu, empty);
     } else {
         int64_t sum = 0;
         bool empty;
-        for (int32_t e = threadIdx.x; e < n; e += blockDim.x) sum += entry_cost(a, e, &empty);
-        write_empty_rows(a);
+        for (int32_t e = threadIdx.x; e < n; e += blockDim.x) {
+            cost = entry_cost(a, e, &empty);
+            sum += cost;
+            busy += cost > 0;
+        }
+        s.any_empty = 1;
         sum = warp_sum(sum);
-        if (lane == 0) red[threadIdx.x >> 5] = sum;
+        busy = __reduce_add_sync(0xffffffffu, busy);
+        const int warps = blockDim.x >> 5;
+        if (lane == 0) red[threadIdx.x >> 5] = sum, red[warps + (threadIdx.x >> 5)] = busy;
         __syncthreads();
-        s.cut.total = 0;
-        for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s.cut.total += red[w];
+        busy = 0;
+        for (int w = 0; w < warps; ++w) total += red[w], busy += (int32_t)red[warps + w];
     }
-    s.cut.per = max(quotient(s.cut.total + a.ctas - 1, a.ctas), (int64_t)a.min_units);
+    // Where runs are longer than a problem's first tile, its beginning counts; shorter runs are best cut
+    // as finely as the tiles are.  Either way a run is as long as any tile, and so, within a problem, holds
+    // a tile's beginning.
+    const int64_t least = a.tile_cost + a.start_cost;
+    s.cut.start = total >= a.ctas * least ? a.start_cost : 0;
+    const int64_t extra = (int64_t)s.cut.start * a.kv_heads;  // of an entry that is busy
+    total += busy * extra;
+    s.cut.per = max(quotient(total + a.ctas - 1, a.ctas), (int64_t)a.tile_cost);
     const int64_t x = blockIdx.x * s.cut.per;
-    s.left = min(s.cut.per, s.cut.total - x);
+    s.left = min(s.cut.per, total - x);
     s.entry = -1;
     s.within = 0;
     if (s.left <= 0) return s;
     int64_t before = 0;
     for (int32_t e0 = 0; e0 < n; e0 += 32) {
         bool empty;
-        if (n > 32) scan = warp_scan(e0 + lane < n ? entry_cost(a, e0 + lane, &empty) : 0);
+        if (n > 32) cost = e0 + lane < n ? entry_cost(a, e0 + lane, &empty) : 0;
+        if (n > 32 || extra != 0) scan = warp_scan(cost + (cost > 0 ? extra : 0));
         const uint32_t past = __ballot_sync(0xffffffffu, before + scan > x);
         if (past) {
             const int first = __ffs(past) - 1;
@@ -202,6 +217,26 @@ __device__ __forceinline__ Start find_start(const AttnArgs& a, int64_t* red) {
         }
         before += __shfl_sync(0xffffffffu, scan, 31);
     }
+    return s;
+}
+
+// The whole block's start.  One warp's work reaches the others through shared memory, so that nothing of
+// it stays in the registers of the loops to come (inlined into each of them, the same code cost the
+// tensor-core kernel 5 % of every tile).
+__device__ __forceinline__ Start block_start(const AttnArgs& a, Start* box, int64_t* red) {
+    if (a.scenes * a.row_tiles > 32 || threadIdx.x / 32 == 2) {  // (warps 0 and 1 have the barriers and tensor memory)
+        const Start s = find_start(a, red);
+        if (threadIdx.x == 64) *box = s;
+    }
+    __syncthreads();
+    Start s;
+    const uint32_t at = smem_u32(box);
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.cut.per) : "r"(at + (uint32_t)offsetof(Start, cut.per)));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.cut.start) : "r"(at + (uint32_t)offsetof(Start, cut.start)));
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.left) : "r"(at + (uint32_t)offsetof(Start, left)));
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.within) : "r"(at + (uint32_t)offsetof(Start, within)));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.entry) : "r"(at + (uint32_t)offsetof(Start, entry)));
+    if (box->any_empty) write_empty_rows(a);
     return s;
 }
 
@@ -219,6 +254,11 @@ struct Segment {
 };
 // Walks the CTA's run; every role of the CTA makes the same walk.  A tile belongs to the run in which
 // its place in the list (cost by cost) begins.
+// Tiles of a problem that begin before place u: the first at 0, tile t at start + t * cost.
+__device__ __forceinline__ int32_t tiles_before(int64_t u, int32_t start, int32_t cost) {
+    const int64_t x = max(u - start, (int64_t)0);
+    return u <= 0 ? 0 : (int32_t)max(cost == 1 ? x : quotient(x + cost - 1, cost), (int64_t)1);
+}
 struct Walk {
     int64_t left, u;  // cost still to come, place within the problem at hand
     int32_t e, h;
@@ -226,7 +266,8 @@ struct Walk {
         if (e < 0) return;
         const int sc = over(e, a.row_tiles), rt = e - sc * a.row_tiles;
         const Scene scene = scene_of(a, sc);
-        const int64_t one = (int64_t)key_tiles(a, scene, rt) * tile_cost(a, valid_rows(a, scene, rt));
+        const int64_t one =
+            s.cut.start + (int64_t)key_tiles(a, scene, rt) * tile_cost(a, valid_rows(a, scene, rt));
         h = s.within < one ? 0 : (int32_t)quotient(s.within, one);
         u = s.within - h * one;
     }
@@ -245,12 +286,12 @@ struct Walk {
                 continue;
             }
             const int32_t cost = tile_cost(a, g->nv);
-            const int64_t u1 = min((int64_t)g->tiles * cost, u + left);
+            const int64_t u1 = min(cut.start + (int64_t)g->tiles * cost, u + left);
             g->h = h;
-            g->t0 = (int32_t)((u + cost - 1) / cost);
-            g->t1 = (int32_t)((u1 + cost - 1) / cost);
-            // the problem's first tile is at this CTA's end - left + 0, its last one (tiles - 1) costs on
-            const int64_t behind = (int64_t)(g->tiles - 1) * cost - left;
+            g->t0 = tiles_before(u, cut.start, cost);
+            g->t1 = tiles_before(u1, cut.start, cost);
+            // the problem's first tile is at this CTA's end - left, and its last one begins so much behind the end
+            const int64_t behind = (g->tiles > 1 ? cut.start + (int64_t)(g->tiles - 1) * cost : 0) - left;
             g->last = u == 0 && behind >= 0 ? (int32_t)(blockIdx.x + 1 + quotient(behind, cut.per)) : -1;
             left -= u1 - u;
             u = 0;
@@ -330,10 +371,11 @@ struct FewLayout {
     static constexpr int kMergeMl = kMergeO + kWarps * kRows * kMergeRow * 4;  // [warp][2][row]
     static constexpr int kBars = kMergeMl + kWarps * 2 * kRows * 4;     // full[], empty[]
     static constexpr int kMeta = kBars + 16 * kStages;                  // per stage: bad sub-pages
-    static constexpr int kMisc = kMeta + 4 * kStages + (kStages & 1 ? 4 : 0);  // abort flag, walk, reduction
-    static constexpr int kEnd = kMisc + 96;
+    static constexpr int kMisc = kMeta + 4 * kStages + (kStages & 1 ? 4 : 0);  // abort flag, reduction[10]
+    static constexpr int kStart = kMisc + 96;
+    static constexpr int kEnd = kStart + sizeof(Start);
     static constexpr int smem_bytes() { return kEnd; }
-    static_assert(kStageBytes % 16 == 0 && kMergeO % 16 == 0 && kBars % 8 == 0 && kMisc % 8 == 0, "alignment");
+    static_assert(kStageBytes % 16 == 0 && kMergeO % 16 == 0 && kBars % 8 == 0 && kMisc % 8 == 0 && kStart % 8 == 0, "alignment");
 };
 
 template <int BITS, int NT>
@@ -345,7 +387,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
     uint64_t* empty = full + L::kStages;
     volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(smem + L::kMeta);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc);
-    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);  // one per warp
+    int64_t* red = reinterpret_cast<int64_t*>(smem + L::kMisc + 8);  // two per warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -356,10 +398,9 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
         *abort_flag = 0;
         fence_barrier_init();
     }
-    const Start start = find_start(a, red);
+    const Start start = block_start(a, reinterpret_cast<Start*>(smem + L::kStart), red);
     const Cut cut = start.cut;
     Walk walk(a, start);
-    __syncthreads();
 
     const int page = 1 << a.page_log2, sub_pages = 128 >> a.page_log2;
     Segment g;

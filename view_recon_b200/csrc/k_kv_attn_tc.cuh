@@ -41,15 +41,16 @@ struct TcLayoutKv {
     static constexpr int kNumBars = 2 * kStages + 2 * 7 + 2;
     static constexpr int kBad = kBars + 8 * kNumBars;      // [stage][8 sub-pages] bytes
     static constexpr int kSeg = kBad + 8 * kStages;        // per half: tiles of the problem at hand, solo flag
-    static constexpr int kMisc = kSeg + 16;                // abort flag, tmem base, reduction[16]
-    static constexpr int kJoin = kMisc + 8 + 128;     // solo: half 1's O [64][128 rows], max, sum (f32)
-    static constexpr int kEnd = kJoin + 66 * 128 * 4;
+    static constexpr int kMisc = kSeg + 16;                // abort flag, tmem base, reduction[32]
+    static constexpr int kJoin = kMisc + 8 + 256;     // solo: half 1's O [64][128 rows], max, sum (f32)
+    static constexpr int kStart = kJoin + 66 * 128 * 4;
+    static constexpr int kEnd = kStart + sizeof(Start);
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t colS(int x) { return 256 * x; }
     static constexpr uint32_t colP(int x) { return 256 * x + 128; }
     static constexpr uint32_t colO(int x) { return 256 * x + 192; }
     static constexpr int smem_bytes() { return 1024 + kEnd; }
-    static_assert(kBars % 8 == 0 && kMisc % 8 == 0, "alignment");
+    static_assert(kBars % 8 == 0 && kMisc % 8 == 0 && kStart % 8 == 0, "alignment");
 };
 
 // Where the pages of a problem are: its row of the page table, its head's page 0, and the tokens that
@@ -213,12 +214,11 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
         tmem_alloc(tmem_base_smem, L::kTmemCols);
         tmem_relinquish();
     }
-    const Start start = find_start(a, red);
+    tc_fence_before();
+    const Start start = block_start(a, reinterpret_cast<Start*>(smem + L::kStart), red);
+    tc_fence_after();
     const Cut cut = start.cut;
     Walk walk(a, start);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = *tmem_base_smem;
     if (threadIdx.x == 64) note_parts(a, cut, walk);  // (of a warp without other work)
     if (start.entry < 0) {  // the whole block: nothing to do

@@ -1376,6 +1376,19 @@ int32_t kv_tile_rows(int64_t rows) {
 // 160 SMs (the workspace's size must not depend on the device that asks).
 int kv_max_ctas(int32_t tile_rows) { return tile_rows == kv::kPairRows ? 160 : 640; }
 
+// What the runs are cut by: about the time of a key tile and of beginning a problem.  tcgen05 kernel: a tile
+// of 256 rows takes 1.9 us of an SM, a problem's beginning (its queries, the first product, its rows out)
+// 6.3 us; a tile of at most 128 rows, which has half the products and exponentials but the whole decoding,
+// 1.5 us in 4 bits and 1.8 in 8.  Without the beginnings in the sum, blocks with many short problems were
+// the last to end: 8 frames at once over themselves (10 992 rows, 16 heads) 609 us, with them 534; ragged
+// frames in 8 bits 167 and 135 us; few rows over ragged scenes 43 and 35 us.
+void kv_costs(int32_t tile_rows, int32_t bits, kv::AttnArgs* a) {
+    const bool pair = tile_rows == kv::kPairRows;
+    a->tile_cost = pair ? 8 : 1;
+    a->solo_cost = pair ? (bits == 4 ? 6 : 7) : 1;
+    a->start_cost = pair ? 28 : 4;
+}
+
 size_t kv_part_bytes(int32_t tile_rows) {
     return align256((size_t)2 * kv_max_ctas(tile_rows) * tile_rows * 64 * 4);
 }
@@ -1578,7 +1591,7 @@ sa_status sa_kv_attn_fwd(const sa_kv_cache* cache, const void* q, int32_t q_head
     a.n_pages = cache->n_pages;
     a.max_pages = cache->max_pages;
     a.frame = frame;
-    a.min_units = a.tile_rows == kv::kPairRows ? kv::kPairCost : 1;  // a run as long as one tile holds one's beginning
+    kv_costs(a.tile_rows, cache->bits, &a);
     a.page_bytes = g.page_bytes;
     a.page_stride = g.page_bytes * cache->heads;
     const float scale = softmax_scale > 0.0f ? softmax_scale : 0.125f;
