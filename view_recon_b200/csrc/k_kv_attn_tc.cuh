@@ -13,8 +13,8 @@
 //   warps 8-15   softmax of half 0, 1: thread r owns row r.  The running maximum is raised (and O
 //                rescaled) only when a score is over it by more than 2^8; P goes to tensor memory as bf16
 // TMEM (512 columns), per half: S 128 (f32), P 64 (bf16 pairs), O 64 (f32).
-// Measured, 16 heads: 1 374 rows over 87 936 tokens in 4 bits 838 us, 590 TFLOP/s (x 4 * 64 FLOP a row and
-// key).  No one unit is full: exponentials 59 % of the XU pipe, tensor pipe 30 %, issue 51 %, DRAM 5 %; each
+// Measured, 16 heads: 1 374 rows over 87 936 tokens in 4 bits 831 us, 596 TFLOP/s (4 * 64 FLOP a row
+// and key).  No one unit is full: exponentials 59 % of the XU pipe, tensor pipe 30 %, issue 51 %, DRAM 5 %; each
 // half's chain (scores, maximum, exponentials, P, product) waits on its own hand-offs, and the other half
 // fills only part of them.  Without any exponential 250 us of 382 (1 280 rows over 43 968 tokens).
 // Other shapes of the same work were slower: 2 blocks an SM of 128 rows with a decode of their own 1039 us,
