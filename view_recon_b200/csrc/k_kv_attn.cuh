@@ -231,11 +231,11 @@ __device__ __forceinline__ Start block_start(const AttnArgs& a, Start* box, int6
     __syncthreads();
     Start s;
     const uint32_t at = smem_u32(box);
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.cut.per) : "r"(at + (uint32_t)offsetof(Start, cut.per)));
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.cut.start) : "r"(at + (uint32_t)offsetof(Start, cut.start)));
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.left) : "r"(at + (uint32_t)offsetof(Start, left)));
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.within) : "r"(at + (uint32_t)offsetof(Start, within)));
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.entry) : "r"(at + (uint32_t)offsetof(Start, entry)));
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.cut.per) : "r"(at + (uint32_t)offsetof(Start, cut.per)) : "memory");
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.cut.start) : "r"(at + (uint32_t)offsetof(Start, cut.start)) : "memory");
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.left) : "r"(at + (uint32_t)offsetof(Start, left)) : "memory");
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.within) : "r"(at + (uint32_t)offsetof(Start, within)) : "memory");
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s.entry) : "r"(at + (uint32_t)offsetof(Start, entry)) : "memory");
     if (box->any_empty) write_empty_rows(a);
     return s;
 }
