@@ -246,3 +246,25 @@ def test_grow_takes_any_integer(lib):
     c.grow(np.int64(3))
     c.grow(np.array([1, 14], dtype=np.int32))
     assert c.lens.tolist() == [4, 17]
+
+
+def test_single_lanes_rejoin_their_warp_before_warp_wide_instructions():
+    """Register splits and tensor-memory accesses (.sync.aligned) want a warp that stands together; where one lane
+    walked alone, or lanes took a branch of their own, a __syncwarp() is what brings it together again.  (Read in
+    the source: no run can be relied on to show the absence.)"""
+    import os
+    import re
+    from view_recon_b200 import _build
+    src = {}
+    for name in ("k_kv_attn.cuh", "k_kv_attn_tc.cuh"):
+        with open(os.path.join(os.path.dirname(_build.__file__), "csrc", name)) as f:
+            src[name] = re.sub(r"//[^\n]*", "", f.read())
+        notes = [m.end() for m in re.finditer(r"if \(threadIdx\.x == \d+\) note_parts\([^;]*;", src[name])]
+        assert len(notes) == 1
+        for at in notes:
+            assert re.match(r"\s*__syncwarp\(\);", src[name][at:]), name
+    softmax = src["k_kv_attn_tc.cuh"]
+    raised = softmax.index("if (mx > m_run + 8.0f)")
+    close = softmax.index("}", raised)
+    assert re.match(r"\s*__syncwarp\(\);", softmax[close + 1:])
+    assert re.search(r"__syncwarp\(\);\s*named_bar_sync\(", src["k_kv_attn.cuh"])

@@ -682,6 +682,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) kv_few_r
                         }
                     }
                 }
+            __syncwarp();  // (the halves of a warp took different rows)
             named_bar_sync(1, 32 * L::kWarps);
         }
     }

@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
     Walk walk(a, start);
     const uint32_t tmem = *tmem_base_smem;
     if (threadIdx.x == 64) note_parts(a, cut, walk);  // (of a warp without other work)
+    __syncwarp();  // the register split below wants whole warps
     if (start.entry < 0) {  // the whole block: nothing to do
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (warp == 1) tmem_dealloc(tmem, L::kTmemCols);
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(512, 1) kv_tc_kernel(const AttnArgs a) {
                     m_run = mx;
                     l_run *= alpha;
                 }
+                __syncwarp();  // the accesses to tensor memory below want whole warps
                 const float m_use = m_run == -INFINITY ? 0.0f : m_run;
                 const float2 mul2 = make_float2(mul, mul), neg2 = make_float2(-m_use, -m_use);
                 float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
