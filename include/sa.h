@@ -374,7 +374,7 @@ typedef struct {
     int32_t heads;      /* key/value heads (>= 1); scenes * heads < 2^31 */
     int32_t head_dim;   /* 64 is built (else SA_ERR_UNSUPPORTED) */
     int32_t page;       /* tokens per page: 16, 32, 64 or 128 */
-    int32_t n_pages;    /* pages of the pool (>= 1) */
+    int32_t n_pages;    /* pages of the pool (>= 1); the pool's bytes < 2^63 */
     int32_t max_pages;  /* columns of the page table (>= 1); max_pages * page <= 2^31 - 256 */
     int32_t bits;       /* 4 or 8 */
 } sa_kv_cache;

@@ -268,3 +268,18 @@ def test_single_lanes_rejoin_their_warp_before_warp_wide_instructions():
     close = softmax.index("}", raised)
     assert re.match(r"\s*__syncwarp\(\);", softmax[close + 1:])
     assert re.search(r"__syncwarp\(\);\s*named_bar_sync\(", src["k_kv_attn.cuh"])
+
+
+def test_pools_past_64_bit_sizes_are_refused(lib):
+    """A pool's size that does not fit 64 bits wrapped round to a small number, and calls took that pool."""
+    from view_recon_b200 import sa
+    top = 2 ** 31 - 1
+    fake = ctypes.c_void_p(0x10000)
+    most = (2 ** 63 - 1) // (128 * 136 * 2 ** 20)        # pages of 2^20 heads that still fit
+    assert sa.sa_kv_pool_size(sa.kv_cache(1, 2 ** 20, most, 5, 128, 8)) == most * 2 ** 20 * 128 * 136
+    for c in (sa.kv_cache(1, top, top, 5, 128, 8), sa.kv_cache(1, 2 ** 20 + 1, most, 5, 128, 8),
+              sa.kv_cache(1, 2 ** 27 + 3, 2 ** 27 + 1, 5, 128, 4)):
+        assert c.n_pages * c.heads * c.page * 2 * (8 * c.bits + 4) >= 2 ** 63
+        assert sa.sa_kv_pool_size(c) == 0
+        assert lib.sa_kv_append(ctypes.byref(c), 1, fake, fake, 0, None, fake, fake, fake, None) == sa.SA_ERR_UNSUPPORTED
+        assert sa.sa_kv_attn_workspace_size(c, c.heads, 1) == 0

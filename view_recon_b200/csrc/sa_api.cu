@@ -1348,6 +1348,8 @@ sa_status kv_geo(const sa_kv_cache* c, KvGeo* g) {
     if ((int64_t)c->scenes * c->heads >= (int64_t(1) << 31)) return SA_ERR_UNSUPPORTED;
     g->page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
     g->page_bytes = (int64_t)c->page * (c->bits == 4 ? kv::Fmt<4>::kTokenBytes : kv::Fmt<8>::kTokenBytes);
+    // places in the pool are 64-bit numbers
+    if ((int64_t)c->n_pages * c->heads > INT64_MAX / g->page_bytes) return SA_ERR_UNSUPPORTED;
     return SA_OK;
 }
 
