@@ -686,3 +686,23 @@ def test_attention_long_runs_of_problems(rows, bits, scenes):
     _attend(p, rng, rows, heads, taken=taken)
     if rows in (20, 300):
         _attend(p, rng, rows, heads, frame=7, taken=taken)
+
+
+def test_rows_without_keys_past_two_to_the_31_pieces():
+    """Empty scenes of so many heads that a row tile's 16-byte pieces of O are more than 2^31: every row gets its
+    zeros.  (Queries and O are one tensor, which rows without keys allow, to hold half the memory.)"""
+    import torch
+    from view_recon_b200 import sa
+    heads, rows = 1 << 20, 256
+    c = sa.kv_cache(1, heads, 1, 1, 16, 4)
+    pool = torch.empty((sa.sa_kv_pool_size(c),), dtype=torch.uint8, device="cuda")
+    o = torch.empty((heads, rows, 64), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((heads, rows), device="cuda")
+    o.fill_(1.0)
+    lse.fill_(1.0)
+    ws = torch.empty((sa.sa_kv_attn_workspace_size(c, heads, rows),), dtype=torch.uint8, device="cuda")
+    table, lens = torch.full((1, 1), -1, dtype=torch.int32, device="cuda"), _counts([0])
+    sa.sa_kv_attn_fwd(c, o, heads, rows, None, 0, 0.0, lens, table, pool, ws, o, lse)
+    _ok()
+    assert all((part == 0).all().item() for part in o.split(1 << 16))
+    assert all(torch.isneginf(part).all().item() for part in lse.split(1 << 18))

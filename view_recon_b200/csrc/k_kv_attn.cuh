@@ -141,8 +141,9 @@ __device__ __forceinline__ void write_empty_rows(const AttnArgs& a) {
         const Scene sc = scene_of(a, s);
         const int32_t nv = valid_rows(a, sc, rt);
         if (nv == 0 || key_tiles(a, sc, rt) > 0) continue;
-        for (int32_t i = threadIdx.x; i < nv * a.kv_heads * 8; i += blockDim.x) {
-            const int32_t x = i / 8 % nv, h = i / 8 / nv;
+        const int64_t pieces = (int64_t)nv * a.kv_heads * 8;  // of 16 bytes (rows are below 2^31, these are not)
+        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
+            const int32_t y = (int32_t)(i / 8), h = y / nv, x = y - h * nv;
             const int64_t row = out_row(a, s, h, rt * a.tile_rows + x);
             reinterpret_cast<uint4*>(a.o + row * 64)[i % 8] = make_uint4(0, 0, 0, 0);
             if (a.lse && i % 8 == 0) a.lse[row] = -INFINITY;
