@@ -283,3 +283,12 @@ def test_pools_past_64_bit_sizes_are_refused(lib):
         assert sa.sa_kv_pool_size(c) == 0
         assert lib.sa_kv_append(ctypes.byref(c), 1, fake, fake, 0, None, fake, fake, fake, None) == sa.SA_ERR_UNSUPPORTED
         assert sa.sa_kv_attn_workspace_size(c, c.heads, 1) == 0
+
+
+def test_a_cache_off_the_gpu_has_no_streams(lib):
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(1, 1, tokens=64, page=16, device="cpu")
+    for call in (lambda: c.grow(1, stream=object()), lambda: c.release(0, stream=object())):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    assert c.lens.tolist() == [0] and c._len == [0]

@@ -706,3 +706,52 @@ def test_rows_without_keys_past_two_to_the_31_pieces():
     _ok()
     assert all((part == 0).all().item() for part in o.split(1 << 16))
     assert all(torch.isneginf(part).all().item() for part in lse.split(1 << 18))
+
+
+def _same(got, ref):
+    """O and LSE of a call within their bars of the oracle's (O, LSE, A, B)."""
+    o, lse = (H.from_device(t) for t in got)
+    ref_o, ref_l, A, B = ref
+    dead = np.isneginf(ref_l)
+    assert (np.abs(o - ref_o) <= _bar(ref_o, A)).all()
+    assert (np.isneginf(lse) == dead).all() and (o[dead] == 0).all()
+    assert (np.abs(lse - ref_l)[~dead] <= (2.0 ** -18 * B + 2.0 ** -20 * (1 + np.abs(ref_l)))[~dead]).all()
+
+
+def test_lengths_and_pages_change_on_the_stream_of_the_calls():
+    """Frames counted in, written and attended to on a side stream, while the current one is far behind."""
+    import torch
+    from view_recon_b200.pipeline import CachedGlobalAttention, FrameCache
+    rng = np.random.default_rng(22)
+    N, heads, steps = 45, 2, 4
+    s = torch.cuda.Stream()
+    rows = [_rows(rng, (heads, N, 64), "bf16") for _ in range(2 * steps)]
+    q, tq = _rows(rng, (heads, 3, 64), "bf16")
+    c = FrameCache(1, heads, tokens=N * steps, page=16)
+    layer = CachedGlobalAttention(c, 3)
+    outs = []
+    torch.cuda.synchronize()
+    for i in range(steps):
+        torch.cuda._sleep(20_000_000)
+        c.grow(N, stream=s)
+        c.append(rows[2 * i][1], rows[2 * i + 1][1], stream=s)
+        layer.forward(tq, stream=s)
+        with torch.cuda.stream(s):
+            outs.append((layer.o.clone(), layer.lse.clone()))
+    c.release(0, stream=s)
+    layer.forward(tq, stream=s)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()      # the current stream is still asleep
+    assert (layer.o == 0).all() and torch.isneginf(layer.lse).all()
+    _ok()
+    for i in range(steps):
+        k = np.concatenate([orc.cache_numbers(rows[2 * j][0], 4) for j in range(i + 1)], 1)
+        v = np.concatenate([orc.cache_numbers(rows[2 * j + 1][0], 4) for j in range(i + 1)], 1)
+        _same(outs[i], orc.cache_attend(q, k, v, 0.125))
+    assert c.lens.tolist() == [0] and (c.page_table == -1).all()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):                 # recorded on the stream that is named
+        with pytest.raises(RuntimeError):
+            c.grow(1, stream=s)
+        torch.zeros(1, device="cuda")
+    assert c._len == [0]

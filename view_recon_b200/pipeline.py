@@ -12,6 +12,7 @@ every step runs in libsa's kernels.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import numbers
@@ -377,7 +378,8 @@ class FrameCache:
     follow them.  The layers of a model see the same tokens: give the second and later layers'
     caches `like=` the first one and they share its lengths, its table and its pages' numbering
     (and only the first one's grow and release are called).  `wrap` adopts tensors that the caller
-    manages.  Calls on one cache are ordered by the caller (one stream, or events).
+    manages.  Calls on one cache, grow and release among them, are ordered by the caller: one stream (each
+    takes `stream=`; without it the device's current one), or events.
     """
 
     def __init__(self, scenes: int, heads: int, tokens: int, n_pages: int | None = None, page: int = 128, bits: int = 4,
@@ -436,14 +438,21 @@ class FrameCache:
         return c
 
     # ---- pages and lengths (host bookkeeping, device tables)
-    def _owned(self):
+    def _owned(self, stream):
+        """Refuse what is not this cache's to change now; returns the context in which its tables are written."""
         if not self._owner:
             raise ValueError("pages and lengths of this cache are managed elsewhere")
-        if self.device.type == "cuda":
-            import torch
-            with torch.cuda.device(self.device):
-                if torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("pages and lengths are the host's: change them outside a recorded graph")
+        if self.device.type != "cuda":
+            if stream is not None:
+                raise ValueError("the cache is not on a CUDA device")
+            return contextlib.nullcontext()
+        import torch
+        if stream is not None and stream.device != self.device:
+            raise ValueError("the stream is on %s, the cache is on %s" % (stream.device, self.device))
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("pages and lengths are the host's: change them outside a recorded graph")
+        return torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream)
 
     def _send(self, values, dtype):
         """Host numbers on the device.  From pinned memory, so that the host does not wait for the work that is
@@ -456,10 +465,11 @@ class FrameCache:
         import torch
         self.lens.copy_(self._send(self._len, torch.int32))
 
-    def grow(self, n):
+    def grow(self, n, stream=None):
         """Count n more tokens (one number, or one per scene) into the cache and give them pages.  Call it once
-        before the layers' appends.  Raises MemoryError, changing nothing, when pages run out."""
-        self._owned()
+        before the layers' appends.  Lengths and table change on `stream` (default: the device's current one),
+        in order with the calls there.  Raises MemoryError, changing nothing, when pages run out."""
+        there = self._owned(stream)
         ns = [int(n)] * self.scenes if isinstance(n, numbers.Integral) else [int(x) for x in n]
         if len(ns) != self.scenes or min(ns) < 0:
             raise ValueError("grow needs one non-negative count, or one per scene")
@@ -477,20 +487,23 @@ class FrameCache:
                 ids.append(self._free.pop())
                 self._pages[s].append(ids[-1])
             self._len[s] += ns[s]
-        if ids:
-            import torch
-            at = self._send([rows, cols, ids], torch.int64)
-            self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
-        self._send_lengths()
+        with there:
+            if ids:
+                import torch
+                at = self._send([rows, cols, ids], torch.int64)
+                self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
+            self._send_lengths()
 
-    def release(self, scene: int):
-        """Drop a scene: its pages are free again and its length is 0."""
-        self._owned()
+    def release(self, scene: int, stream=None):
+        """Drop a scene: its pages are free again and its length is 0, for what follows on `stream` (default:
+        the device's current one)."""
+        there = self._owned(stream)
         self._free.extend(reversed(self._pages[scene]))
         self._pages[scene] = []
         self._len[scene] = 0
-        self.page_table[scene].fill_(-1)
-        self._send_lengths()
+        with there:
+            self.page_table[scene].fill_(-1)
+            self._send_lengths()
 
     # ---- rows (each one C call)
     def _counts(self, name, t):
