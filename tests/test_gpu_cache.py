@@ -755,3 +755,40 @@ def test_lengths_and_pages_change_on_the_stream_of_the_calls():
             c.grow(1, stream=s)
         torch.zeros(1, device="cuda")
     assert c._len == [0]
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_tensors_of_calls_on_a_side_stream_live_until_they_have_run(rows):
+    """Rows, queries, counts and a layer's workspace dropped right after a call that is still queued on another
+    stream: their memory is not handed out again before it has run."""
+    import torch
+    from view_recon_b200.pipeline import CachedGlobalAttention
+    rng = np.random.default_rng(23)
+    p = Pool(rng, [20000], 2, 64, 4)
+    _fill(p, rng)
+    k, tk = _rows(rng, (2, 300, 64), "bf16")
+    v, tv = _rows(rng, (2, 300, 64), "bf16")
+    q, tq = _rows(rng, (2, rows, 64), "bf16")
+    tn, tm = _counts([300]), _counts([rows])
+    s = torch.cuda.Stream()
+    for cycles in (1000, 200_000_000):   # once to have memory and kernels loaded: getting those waits for the device
+        a, b, n, x, m = (t.clone() for t in (tk, tv, tn, tq, tm))
+        layer = CachedGlobalAttention(p.cache, rows)
+        o, lse, size = layer.o, layer.lse, layer.ws.numel()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(cycles)
+        p.cache.append(a, b, new_len=n, stream=s)
+        layer.forward(x, q_len=m, stream=s)
+        del a, b, n, x, m, layer
+        junk = [torch.full_like(t, 7) for _ in range(8) for t in (tk, tq, tn)]
+        junk += [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        torch.cuda.current_stream().synchronize()
+        ahead = not s.query()
+        _ok()
+        K, V = p.rows(0)
+        assert np.array_equal(K[:, 19700:], orc.cache_numbers(k, 4))
+        assert np.array_equal(V[:, 19700:], orc.cache_numbers(v, 4))
+        _same((o, lse), orc.cache_attend(q, K, V, 0.125))
+        del junk
+    assert ahead                         # all of that came before the calls

@@ -493,6 +493,8 @@ class FrameCache:
                 at = self._send([rows, cols, ids], torch.int64)
                 self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
             self._send_lengths()
+        if stream is not None:
+            self._hold(stream)
 
     def release(self, scene: int, stream=None):
         """Drop a scene: its pages are free again and its length is 0, for what follows on `stream` (default:
@@ -504,6 +506,8 @@ class FrameCache:
         with there:
             self.page_table[scene].fill_(-1)
             self._send_lengths()
+        if stream is not None:
+            self._hold(stream)
 
     # ---- rows (each one C call)
     def _counts(self, name, t):
@@ -523,6 +527,13 @@ class FrameCache:
         if st != sa.SA_OK:
             raise sa.SaError(fn.__name__, st, sa.status_string(st))
 
+    def _hold(self, stream, *tensors):
+        """Tensors of a call that is queued on a stream that is named: their memory is not handed out again before
+        the stream has come past it, whoever drops them."""
+        for t in (*tensors, self.pool, self.page_table, self.lens):
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
     def append(self, k, v, new_len=None, stream=None):
         """Write rows k, v [scenes * heads][n][64] (bf16 or f32) as the last n tokens of every scene; with
         new_len (int32 device tensor [scenes]) only the first new_len[s] rows, as the last new_len[s] tokens."""
@@ -535,6 +546,8 @@ class FrameCache:
         self._call(sa.load().sa_kv_append, sa.SA_BF16 if k.dtype is self._types[0] else sa.SA_F32, pk, pv, n,
                    self._counts("new_len", new_len), self.lens.data_ptr(), self.page_table.data_ptr(),
                    self.pool.data_ptr(), stream=stream)
+        if stream is not None:
+            self._hold(stream, k, v, new_len)
 
     def read(self, k=None, v=None, start=None, n_len=None, stream=None):
         """Fill k and v [scenes * heads][n][64] (bf16 or f32, either may be None) with the tokens from start[s]
@@ -550,6 +563,8 @@ class FrameCache:
             self._call(sa.load().sa_kv_read, sa.SA_BF16 if ref.dtype is self._types[0] else sa.SA_F32, n,
                        self._counts("n_len", n_len), self._counts("start", start), self.lens.data_ptr(),
                        self.page_table.data_ptr(), self.pool.data_ptr(), pk, pv, stream=stream)
+            if stream is not None:
+                self._hold(stream, k, v, start, n_len)
         return k, v
 
 
@@ -587,6 +602,8 @@ class CachedGlobalAttention:
         c._call(sa.load().sa_kv_attn_fwd, pq, self.q_heads, self.rows, c._counts("q_len", q_len), self.frame,
                 self.softmax_scale, c.lens.data_ptr(), c.page_table.data_ptr(), c.pool.data_ptr(), self.ws.data_ptr(),
                 self.ws.numel(), self.o.data_ptr(), None if self.lse is None else self.lse.data_ptr(), stream=stream)
+        if stream is not None:
+            c._hold(stream, q, q_len, self.ws, self.o, self.lse)
         return self.o, self.lse
 
     __call__ = forward
