@@ -292,3 +292,46 @@ def test_a_cache_off_the_gpu_has_no_streams(lib):
         with pytest.raises(ValueError, match="CUDA"):
             call()
     assert c.lens.tolist() == [0] and c._len == [0]
+
+
+def test_rows_that_grow_did_not_count_in_are_refused(lib):
+    """Without new_len every scene's last n tokens are written: n has to be what grow counted into each of them.
+    (Off the GPU a call that passes this check ends at the next one.)"""
+    import torch
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(2, 1, tokens=200, page=16, device="cpu")
+    layers = [c, FrameCache(2, 1, tokens=200, page=16, bits=8, like=c)]
+
+    def check(n, good, **kw):
+        x = torch.zeros(2, n, 64)
+        for layer in layers:
+            with pytest.raises(ValueError, match="CUDA" if good else "grow counted"):
+                layer.append(x, x, **kw)
+
+    check(3, False)                                       # nothing counted in
+    c.grow(5)
+    check(4, False)
+    check(6, False)
+    check(5, True)
+    check(5, True)                                        # the same rows once more
+    c.grow([3, 0])
+    check(3, False)                                       # the second scene's last rows are old ones
+    check(5, False)
+    check(3, True, new_len=torch.tensor([3, 0], dtype=torch.int32))
+    c.grow(2)
+    check(2, True)
+    c.grow(4)
+    c.grow(3)                                             # two frames, written at once or the second alone
+    check(7, True)
+    check(3, True)
+    check(4, False)
+    c.grow(3)
+    check(3, True)
+    check(10, False)                                      # the seven were written
+    c.release(1)
+    check(3, False)
+    c.grow([0, 3])
+    check(3, False)
+    c.grow([6, 3])
+    check(6, True)                                        # nothing written since: 6 and 6
+    layers[1].append(torch.empty(2, 0, 64), torch.empty(2, 0, 64))

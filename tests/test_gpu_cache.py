@@ -792,3 +792,50 @@ def test_tensors_of_calls_on_a_side_stream_live_until_they_have_run(rows):
         _same((o, lse), orc.cache_attend(q, K, V, 0.125))
         del junk
     assert ahead                         # all of that came before the calls
+
+
+@pytest.mark.parametrize("rows", [2, 60])
+def test_recorded_writes_and_calls_follow_the_cache(rows):
+    """One graph that writes a frame, attends to the cache and reads the frame back, replayed as frames come, a
+    scene is dropped and its pages are used again: O, LSE and the rows at every step."""
+    import torch
+    from view_recon_b200.pipeline import CachedGlobalAttention, FrameCache
+    rng = np.random.default_rng(24)
+    N, heads = 70, 2
+    c = FrameCache(2, heads, tokens=5 * N, n_pages=34, page=16, bits=8)
+    layer = CachedGlobalAttention(c, rows, q_heads=2 * heads)
+    tk, tv, out = (torch.zeros((2 * heads, N, 64), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    tq = torch.zeros((4 * heads, rows, 64), dtype=torch.bfloat16, device="cuda")
+    c.grow(N)
+    c.append(tk, tv)
+    layer.forward(tq)
+    c.read(v=out)
+    c.release(0)
+    c.release(1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(tk, tv)
+        layer.forward(tq)
+        c.read(v=out)
+    K, V = ([np.zeros((heads, 0, 64))] * 2 for _ in range(2))
+    for step in range(7):
+        if step in (3, 5):
+            s = step // 2 - 1
+            c.release(s)
+            K[s] = V[s] = np.zeros((heads, 0, 64))
+        c.grow(N)
+        k, new_k = _rows(rng, tuple(tk.shape), "bf16")
+        v, new_v = _rows(rng, tuple(tv.shape), "bf16")
+        q, new_q = _rows(rng, tuple(tq.shape), "bf16")
+        for a, b in ((tk, new_k), (tv, new_v), (tq, new_q)):
+            a.copy_(b)
+        g.replay()
+        _ok()
+        assert np.array_equal(H.from_device(out), orc.cache_numbers(v, 8))
+        for s in range(2):
+            mine = slice(s * heads, (s + 1) * heads)
+            K[s] = np.concatenate([K[s], orc.cache_numbers(k[mine], 8)], 1)
+            V[s] = np.concatenate([V[s], orc.cache_numbers(v[mine], 8)], 1)
+            mine = slice(2 * s * heads, 2 * (s + 1) * heads)
+            _same((layer.o[mine], layer.lse[mine]), orc.cache_attend(q[mine], K[s], V[s], 0.125))

@@ -362,6 +362,26 @@ def _want(name, t, shape, dtypes, device, align=16):
     raise ValueError("%s does not start on a %d-byte boundary" % (name, align))
 
 
+class _Counted:
+    """What grow has counted into the scenes, shared by the caches of a model's layers: the last grow's counts, and
+    those of all grows since the last append."""
+
+    def __init__(self, scenes):
+        self.last, self.open, self.appended, self.fits = [0] * scenes, [0] * scenes, False, ()
+
+    def grow(self, ns):
+        self.open = [m if self.appended else o + m for o, m in zip(self.open, ns)]
+        self.last, self.appended = list(ns), False
+        self._settle()
+
+    def release(self, scene):
+        self.last[scene] = self.open[scene] = 0
+        self._settle()
+
+    def _settle(self):
+        self.fits = tuple(x[0] for x in (self.last, self.open) if min(x) == max(x))  # counts that suit every scene
+
+
 class FrameCache:
     """K and V of the frames seen so far, of one layer, held in 4 or 8 bits in pages.
 
@@ -400,13 +420,14 @@ class FrameCache:
         self.pool = torch.empty((self.pool_bytes,), dtype=torch.uint8, device=dev)
         self._owner = like is None
         if like is not None:
-            self.page_table, self.lens = like.page_table, like.lens
+            self.page_table, self.lens, self._news = like.page_table, like.lens, like._news
             return
         self.page_table = torch.full((scenes, max_pages), -1, dtype=torch.int32, device=dev)
         self.lens = torch.zeros((scenes,), dtype=torch.int32, device=dev)
         self._len = [0] * scenes              # host copies: the pages' bookkeeping is the host's
         self._pages = [[] for _ in range(scenes)]
         self._free = list(range(n_pages - 1, -1, -1))
+        self._news = _Counted(scenes)
 
     def _describe(self, scenes, heads, n_pages, max_pages, page, bits, head_dim, device):
         self.desc = sa.kv_cache(scenes, heads, n_pages, max_pages, page, bits, head_dim)
@@ -434,7 +455,7 @@ class FrameCache:
         _want("pool", pool, (c.n_pages, c.heads, per_page), (torch.uint8,), pool.device)
         _want("page_table", page_table, (c.scenes, c.max_pages), (torch.int32,), pool.device, 4)
         _want("lens", lens, (c.scenes,), (torch.int32,), pool.device, 4)
-        c.pool, c.page_table, c.lens, c._owner = pool, page_table, lens, False
+        c.pool, c.page_table, c.lens, c._owner, c._news = pool, page_table, lens, False, None
         return c
 
     # ---- pages and lengths (host bookkeeping, device tables)
@@ -449,9 +470,8 @@ class FrameCache:
         import torch
         if stream is not None and stream.device != self.device:
             raise ValueError("the stream is on %s, the cache is on %s" % (stream.device, self.device))
-        with torch.cuda.device(self.device), torch.cuda.stream(stream):
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("pages and lengths are the host's: change them outside a recorded graph")
+        if self._recording(stream):
+            raise RuntimeError("pages and lengths are the host's: change them outside a recorded graph")
         return torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream)
 
     def _send(self, values, dtype):
@@ -487,6 +507,7 @@ class FrameCache:
                 ids.append(self._free.pop())
                 self._pages[s].append(ids[-1])
             self._len[s] += ns[s]
+        self._news.grow(ns)
         with there:
             if ids:
                 import torch
@@ -503,6 +524,7 @@ class FrameCache:
         self._free.extend(reversed(self._pages[scene]))
         self._pages[scene] = []
         self._len[scene] = 0
+        self._news.release(scene)
         with there:
             self.page_table[scene].fill_(-1)
             self._send_lengths()
@@ -527,6 +549,13 @@ class FrameCache:
         if st != sa.SA_OK:
             raise sa.SaError(fn.__name__, st, sa.status_string(st))
 
+    def _recording(self, stream):
+        import torch
+        if self.device.type != "cuda":
+            return False
+        with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
     def _hold(self, stream, *tensors):
         """Tensors of a call that is queued on a stream that is named: their memory is not handed out again before
         the stream has come past it, whoever drops them."""
@@ -536,13 +565,22 @@ class FrameCache:
 
     def append(self, k, v, new_len=None, stream=None):
         """Write rows k, v [scenes * heads][n][64] (bf16 or f32) as the last n tokens of every scene; with
-        new_len (int32 device tensor [scenes]) only the first new_len[s] rows, as the last new_len[s] tokens."""
+        new_len (int32 device tensor [scenes]) only the first new_len[s] rows, as the last new_len[s] tokens.
+        Without new_len, n has to be what the last grow counted into every scene, or what the grows since the last
+        append did together: other rows would go over tokens that were there before, or leave new ones unwritten.
+        (Not asked of caches that the caller manages, nor while a graph is recorded, whose replays have their own
+        grows.)"""
         n = k.shape[1] if k.dim() == 3 else -1
         shape = (self.scenes * self.heads, n, self.d)
         pk = _want("k", k, shape, self._types, self.device)
         pv = _want("v", v, shape, (k.dtype,), self.device)
         if n == 0:
             return
+        if self._news is not None:
+            if new_len is None and n not in self._news.fits and not self._recording(stream):
+                raise ValueError("%d rows for every scene, but the last grow counted in %s: rows of other counts "
+                                 "need new_len" % (n, self._news.last))
+            self._news.appended = True
         self._call(sa.load().sa_kv_append, sa.SA_BF16 if k.dtype is self._types[0] else sa.SA_F32, pk, pv, n,
                    self._counts("new_len", new_len), self.lens.data_ptr(), self.page_table.data_ptr(),
                    self.pool.data_ptr(), stream=stream)
