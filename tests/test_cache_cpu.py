@@ -335,3 +335,26 @@ def test_rows_that_grow_did_not_count_in_are_refused(lib):
     c.grow([6, 3])
     check(6, True)                                        # nothing written since: 6 and 6
     layers[1].append(torch.empty(2, 0, 64), torch.empty(2, 0, 64))
+
+
+def test_binding_refuses_other_types(lib):
+    """An LSE of a smaller type would be written past its end, lengths of another would be read as nonsense."""
+    import torch
+    from view_recon_b200 import sa
+    c = sa.kv_cache(1, 1, 4, 4)
+    x, i = torch.zeros(1, 3, 64), torch.zeros(4, dtype=torch.int32)
+    h = x.bfloat16()
+    for n_len, lens, table in ((None, x, i), (None, i, i.long()), (i.long(), i, i)):
+        with pytest.raises(ValueError, match="int32"):
+            sa.sa_kv_append(c, x, x, 3, n_len, lens, table, x)
+        with pytest.raises(ValueError, match="int32"):
+            sa.sa_kv_read(c, 3, n_len, None, lens, table, x, x, x)
+        with pytest.raises(ValueError, match="int32"):
+            sa.sa_kv_attn_fwd(c, h, 1, 3, n_len, 0, 0.0, lens, table, x, x, h)
+    with pytest.raises(ValueError, match="int32"):
+        sa.sa_kv_read(c, 3, None, x, i, i, x, x, x)
+    for q, o, lse in ((x, h, None), (h, x, None), (h, h, h), (h.half(), h, x)):
+        with pytest.raises(ValueError, match="bf16"):
+            sa.sa_kv_attn_fwd(c, q, 1, 3, None, 0, 0.0, i, i, x, x, o, lse)
+    with pytest.raises(ValueError, match="CUDA"):
+        sa.sa_kv_attn_fwd(c, h, 1, 3, None, 0, 0.0, i, i, x, x, h, x)

@@ -839,3 +839,47 @@ def test_recorded_writes_and_calls_follow_the_cache(rows):
             V[s] = np.concatenate([V[s], orc.cache_numbers(v[mine], 8)], 1)
             mine = slice(2 * s * heads, 2 * (s + 1) * heads)
             _same((layer.o[mine], layer.lse[mine]), orc.cache_attend(q[mine], K[s], V[s], 0.125))
+
+
+@pytest.mark.parametrize("rows", [4, 100])
+def test_binding_calls_and_layer_objects_agree(rows):
+    """The thin binding's three calls, with scenes that share their first pages, and no LSE asked for."""
+    import torch
+    from view_recon_b200 import sa
+    from view_recon_b200.pipeline import CachedGlobalAttention, FrameCache
+    rng = np.random.default_rng(25)
+    page, heads = 32, 2
+    table = torch.tensor([[4, 0, 2], [4, 0, 3]], dtype=torch.int32, device="cuda")
+    lens = _counts([90, 70])
+    pools = [torch.zeros((5, heads, page * 72), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    caches = [FrameCache.wrap(p, table, lens, page=page) for p in pools]
+    desc = caches[0].desc
+    first, first_k = _rows(rng, (2 * heads, 64, 64), "f32")
+    k, tk = _rows(rng, (2 * heads, 26, 64), "f32")
+    shared = _counts([64, 64])
+    own = _counts([26, 6])
+    sa.sa_kv_append(desc, first_k, first_k, 64, _counts([64, 0]), shared, table, pools[0])   # the shared pages, once
+    sa.sa_kv_append(desc, tk, tk, 26, own, lens, table, pools[0])
+    whole = FrameCache.wrap(pools[1], table, shared, page=page)
+    whole.append(first_k, first_k, new_len=_counts([64, 0]))
+    caches[1].append(tk, tk, new_len=own)
+    _ok()
+    assert torch.equal(*pools)
+    a, b = (torch.zeros((2 * heads, 26, 64), device="cuda") for _ in range(2))
+    sa.sa_kv_read(desc, 26, own, None, lens, table, pools[0], None, a)
+    caches[1].read(v=b, n_len=own)
+    q, tq = _rows(rng, (2 * heads, rows, 64), "bf16")
+    ws = torch.empty((sa.sa_kv_attn_workspace_size(desc, heads, rows),), dtype=torch.uint8, device="cuda")
+    o = torch.zeros((2 * heads, rows, 64), dtype=torch.bfloat16, device="cuda")
+    sa.sa_kv_attn_fwd(desc, tq, heads, rows, None, 0, 0.0, lens, table, pools[0], ws, o)
+    plain = CachedGlobalAttention(caches[1], rows, with_lse=False)
+    got, none = plain.forward(tq)
+    layer = CachedGlobalAttention(caches[1], rows)
+    layer.forward(tq)
+    _ok()
+    assert none is None and torch.equal(a, b) and torch.equal(o, got) and torch.equal(o, layer.o)
+    for s, m in ((0, 26), (1, 6)):
+        K = np.concatenate([orc.cache_numbers(first[:heads], 4),
+                            orc.cache_numbers(k[s * heads:(s + 1) * heads, :m], 4)], 1)
+        mine = slice(s * heads, (s + 1) * heads)
+        _same((layer.o[mine], layer.lse[mine]), orc.cache_attend(q[mine], K, K, 0.125))

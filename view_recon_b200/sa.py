@@ -299,6 +299,12 @@ def _dtype_of(t) -> int:
     raise ValueError("expected a bf16 or f32 tensor")
 
 
+def _counts(*tensors):
+    import torch
+    if any(t is not None and t.dtype != torch.int32 for t in tensors):
+        raise ValueError("lengths, counts and page tables are int32 tensors")
+
+
 def raw_stream(device_index: int, stream=None) -> int:
     """Handle of a torch stream, or of the device's current one."""
     if stream is not None:
@@ -318,6 +324,7 @@ def sa_kv_append(cache, k, v, n, n_len, lens, page_table, pool, stream=None):
     """k, v: [scenes * heads][n][64], both bf16 or both f32; n_len: int32 device tensor [scenes] or None."""
     if k.dtype != v.dtype:
         raise ValueError("k and v differ in type")
+    _counts(n_len, lens, page_table)
     st = load().sa_kv_append(ctypes.byref(cache), _dtype_of(k), _ptr(k), _ptr(v), int(n), _ptr(n_len), _ptr(lens),
                              _ptr(page_table), _ptr(pool), _stream(stream))
     _check("sa_kv_append", st)
@@ -329,6 +336,7 @@ def sa_kv_read(cache, n, n_len, start, lens, page_table, pool, k, v, stream=None
         raise ValueError("nothing to read into")
     if k is not None and v is not None and k.dtype != v.dtype:
         raise ValueError("k and v differ in type")
+    _counts(n_len, start, lens, page_table)
     st = load().sa_kv_read(ctypes.byref(cache), _dtype_of(k if k is not None else v), int(n), _ptr(n_len), _ptr(start),
                            _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(k), _ptr(v), _stream(stream))
     _check("sa_kv_read", st)
@@ -340,6 +348,12 @@ def sa_kv_attn_workspace_size(cache, q_heads, rows) -> int:
 
 def sa_kv_attn_fwd(cache, q, q_heads, rows, q_len, frame, softmax_scale, lens, page_table, pool, workspace, o, lse=None,
                    stream=None):
+    """q, o: [scenes * q_heads][rows][64] bf16; lse: f32 [scenes * q_heads][rows] or None; q_len: int32 device tensor
+    [scenes] or None."""
+    import torch
+    if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16 or (lse is not None and lse.dtype != torch.float32):
+        raise ValueError("q and o are bf16 tensors, lse an f32 one")
+    _counts(q_len, lens, page_table)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = load().sa_kv_attn_fwd(ctypes.byref(cache), _ptr(q), int(q_heads), int(rows), _ptr(q_len), int(frame),
                                float(softmax_scale), _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(workspace),
