@@ -358,3 +358,34 @@ def test_binding_refuses_other_types(lib):
             sa.sa_kv_attn_fwd(c, q, 1, 3, None, 0, 0.0, i, i, x, x, o, lse)
     with pytest.raises(ValueError, match="CUDA"):
         sa.sa_kv_attn_fwd(c, h, 1, 3, None, 0, 0.0, i, i, x, x, h, x)
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """ctypes cuts an integer to the low bits of its argument: 2^32 + 1 scenes were one, a frame of 2^32 + 7 tokens
+    seven."""
+    import torch
+    from view_recon_b200 import sa
+    from view_recon_b200.pipeline import CachedGlobalAttention, FrameCache
+    big = 2 ** 32
+    for args in ((big + 1, 1, 4, 4), (1, big + 1, 4, 4), (1, 1, big + 4, 4), (1, 1, 4, big + 4), (2 ** 31, 1, 4, 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sa.kv_cache(*args)
+    with pytest.raises(ValueError, match="32 bits"):
+        sa.kv_cache(1, 1, 4, 4, bits=big + 4)
+    c = sa.kv_cache(1, 1, 4, 4)
+    for heads, rows in ((1, big + 5), (big + 1, 5)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sa.sa_kv_attn_workspace_size(c, heads, rows)
+    i, x = torch.zeros(4, dtype=torch.int32), torch.zeros(1, 3, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        sa.sa_kv_attn_fwd(c, x.bfloat16(), 1, 3, None, big + 7, 0.0, i, i, x, x, x.bfloat16())
+    for kw in (dict(scenes=big + 1), dict(heads=big + 1), dict(tokens=128 * (big + 1)), dict(n_pages=big + 1)):
+        with pytest.raises(ValueError):
+            FrameCache(**{**dict(scenes=1, heads=1, tokens=128, device="cpu"), **kw})
+    cache = FrameCache(1, 1, tokens=128, device="cpu")
+    for frame in (-1, 2 ** 31, big + 7):
+        with pytest.raises(ValueError, match="frame"):
+            CachedGlobalAttention(cache, 2, frame=frame)
+    with pytest.raises(ValueError, match="32 bits"):
+        CachedGlobalAttention(cache, big + 2)
+    assert CachedGlobalAttention(cache, 2, frame=2 ** 31 - 1).frame == 2 ** 31 - 1

@@ -626,6 +626,8 @@ class CachedGlobalAttention:
         nbytes = sa.sa_kv_attn_workspace_size(cache.desc, self.q_heads, self.rows)
         if nbytes == 0:
             raise ValueError("q_heads is a multiple of the cache's heads and rows is positive")
+        if not 0 <= self.frame < 2 ** 31:
+            raise ValueError("frame is 0 or a frame's tokens, below 2^31")
         bh, dev = cache.scenes * self.q_heads, cache.device
         self._q_shape = (bh, self.rows, cache.d)
         self.ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)

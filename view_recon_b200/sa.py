@@ -286,8 +286,16 @@ def sa_sga_fwd(shp, grid_h, grid_w, s_h, s_w, q, k, v, workspace, o, lse=None, s
 # ------------------------------------------------------------------------- the frame cache
 
 
+def _i32(*values):
+    """Integers for int32 arguments; ctypes would cut larger ones to their low bits."""
+    values = [int(x) for x in values]
+    if any(x < -2 ** 31 or x >= 2 ** 31 for x in values):
+        raise ValueError("%s: an argument does not fit 32 bits" % values)
+    return values
+
+
 def kv_cache(scenes, heads, n_pages, max_pages, page=128, bits=4, head_dim=64) -> SaKvCache:
-    return SaKvCache(int(scenes), int(heads), int(head_dim), int(page), int(n_pages), int(max_pages), int(bits))
+    return SaKvCache(*_i32(scenes, heads, head_dim, page, n_pages, max_pages, bits))
 
 
 def _dtype_of(t) -> int:
@@ -325,7 +333,7 @@ def sa_kv_append(cache, k, v, n, n_len, lens, page_table, pool, stream=None):
     if k.dtype != v.dtype:
         raise ValueError("k and v differ in type")
     _counts(n_len, lens, page_table)
-    st = load().sa_kv_append(ctypes.byref(cache), _dtype_of(k), _ptr(k), _ptr(v), int(n), _ptr(n_len), _ptr(lens),
+    st = load().sa_kv_append(ctypes.byref(cache), _dtype_of(k), _ptr(k), _ptr(v), *_i32(n), _ptr(n_len), _ptr(lens),
                              _ptr(page_table), _ptr(pool), _stream(stream))
     _check("sa_kv_append", st)
 
@@ -337,13 +345,13 @@ def sa_kv_read(cache, n, n_len, start, lens, page_table, pool, k, v, stream=None
     if k is not None and v is not None and k.dtype != v.dtype:
         raise ValueError("k and v differ in type")
     _counts(n_len, start, lens, page_table)
-    st = load().sa_kv_read(ctypes.byref(cache), _dtype_of(k if k is not None else v), int(n), _ptr(n_len), _ptr(start),
+    st = load().sa_kv_read(ctypes.byref(cache), _dtype_of(k if k is not None else v), *_i32(n), _ptr(n_len), _ptr(start),
                            _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(k), _ptr(v), _stream(stream))
     _check("sa_kv_read", st)
 
 
 def sa_kv_attn_workspace_size(cache, q_heads, rows) -> int:
-    return int(load().sa_kv_attn_workspace_size(ctypes.byref(cache), int(q_heads), int(rows)))
+    return int(load().sa_kv_attn_workspace_size(ctypes.byref(cache), *_i32(q_heads, rows)))
 
 
 def sa_kv_attn_fwd(cache, q, q_heads, rows, q_len, frame, softmax_scale, lens, page_table, pool, workspace, o, lse=None,
@@ -355,7 +363,8 @@ def sa_kv_attn_fwd(cache, q, q_heads, rows, q_len, frame, softmax_scale, lens, p
         raise ValueError("q and o are bf16 tensors, lse an f32 one")
     _counts(q_len, lens, page_table)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load().sa_kv_attn_fwd(ctypes.byref(cache), _ptr(q), int(q_heads), int(rows), _ptr(q_len), int(frame),
+    q_heads, rows, frame = _i32(q_heads, rows, frame)
+    st = load().sa_kv_attn_fwd(ctypes.byref(cache), _ptr(q), q_heads, rows, _ptr(q_len), frame,
                                float(softmax_scale), _ptr(lens), _ptr(page_table), _ptr(pool), _ptr(workspace),
                                ws_bytes, _ptr(o), _ptr(lse), _stream(stream))
     _check("sa_kv_attn_fwd", st)
