@@ -389,3 +389,31 @@ def test_sizes_past_32_bits_are_refused(lib):
     with pytest.raises(ValueError, match="32 bits"):
         CachedGlobalAttention(cache, big + 2)
     assert CachedGlobalAttention(cache, 2, frame=2 ** 31 - 1).frame == 2 ** 31 - 1
+
+
+def test_a_failed_send_leaves_the_books_as_they_were(lib, monkeypatch):
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(2, 1, tokens=64, n_pages=6, page=16, device="cpu")
+    c.grow([20, 3])
+    books = lambda: (c._len[:], [p[:] for p in c._pages], c._free[:], c.lens.tolist(), list(c._news.last))  # noqa: E731
+    before, send = books(), c._send
+    for failing in (1, 2):                                 # the pages' copy, or the lengths'
+        calls = []
+
+        def fail(values, dtype):
+            calls.append(0)
+            if len(calls) == failing:
+                raise RuntimeError("no memory")
+            return send(values, dtype)
+
+        monkeypatch.setattr(c, "_send", fail)
+        with pytest.raises(RuntimeError, match="no memory"):
+            c.grow([20, 0])
+        assert books() == before
+    monkeypatch.setattr(c, "_send", send)
+    c.grow([44, 29])                                       # all six pages, each once
+    used = [p for pages in c._pages for p in pages]
+    assert sorted(used) == list(range(6)) and c._free == [] and c.lens.tolist() == [64, 32]
+    assert [x for x in c.page_table.flatten().tolist() if x >= 0] == used
+    c.release(0)
+    assert sorted(c._free) == sorted(set(range(6)) - set(c._pages[1])) and c.lens.tolist() == [0, 32]

@@ -481,39 +481,40 @@ class FrameCache:
         pin = self.device.type == "cuda"
         return torch.tensor(values, dtype=dtype, pin_memory=pin).to(self.device, non_blocking=pin)
 
-    def _send_lengths(self):
+    def _send_lengths(self, lens):
         import torch
-        self.lens.copy_(self._send(self._len, torch.int32))
+        self.lens.copy_(self._send(lens, torch.int32))
 
     def grow(self, n, stream=None):
         """Count n more tokens (one number, or one per scene) into the cache and give them pages.  Call it once
         before the layers' appends.  Lengths and table change on `stream` (default: the device's current one),
         in order with the calls there.  Raises MemoryError, changing nothing, when pages run out."""
         there = self._owned(stream)
-        ns = [int(n)] * self.scenes if isinstance(n, numbers.Integral) else [int(x) for x in n]
+        ns = [n] * self.scenes if isinstance(n, numbers.Integral) else [int(x) for x in n]
         if len(ns) != self.scenes or min(ns) < 0:
             raise ValueError("grow needs one non-negative count, or one per scene")
-        need = [-(-(self._len[s] + ns[s]) // self.page) for s in range(self.scenes)]
-        if max(need) > self.max_pages:
+        lens = [have + int(x) for have, x in zip(self._len, ns)]
+        if max(lens) > self.max_pages * self.page:
             raise ValueError("a scene is longer than its row of the page table")
-        more = [need[s] - len(self._pages[s]) for s in range(self.scenes)]
-        if sum(more) > len(self._free):
+        more = [-(-new // self.page) - len(have) for new, have in zip(lens, self._pages)]
+        free = len(self._free) - sum(more)
+        if free < 0:
             raise MemoryError("%d more pages needed, %d free" % (sum(more), len(self._free)))
-        rows, cols, ids = [], [], []
-        for s in range(self.scenes):
-            for _ in range(more[s]):
-                rows.append(s)
-                cols.append(len(self._pages[s]))
-                ids.append(self._free.pop())
-                self._pages[s].append(ids[-1])
-            self._len[s] += ns[s]
-        self._news.grow(ns)
+        ids = self._free[:free - 1 if free else None:-1]  # from the end
+        rows = [s for s in range(self.scenes) for _ in range(more[s])]
+        cols = [len(self._pages[s]) + i for s in range(self.scenes) for i in range(more[s])]
         with there:
             if ids:
                 import torch
                 at = self._send([rows, cols, ids], torch.int64)
                 self.page_table.index_put_((at[0], at[1]), at[2].to(torch.int32))
-            self._send_lengths()
+            self._send_lengths(lens)
+        # the host's books last: what fails above (memory, the device) has changed nothing that a call reads
+        del self._free[free:]
+        for s, page in zip(rows, ids):
+            self._pages[s].append(page)
+        self._len = lens
+        self._news.grow([int(x) for x in ns])
         if stream is not None:
             self._hold(stream)
 
@@ -521,13 +522,15 @@ class FrameCache:
         """Drop a scene: its pages are free again and its length is 0, for what follows on `stream` (default:
         the device's current one)."""
         there = self._owned(stream)
-        self._free.extend(reversed(self._pages[scene]))
-        self._pages[scene] = []
-        self._len[scene] = 0
-        self._news.release(scene)
+        lens = list(self._len)
+        lens[scene] = 0
         with there:
             self.page_table[scene].fill_(-1)
-            self._send_lengths()
+            self._send_lengths(lens)
+        self._free.extend(reversed(self._pages[scene]))
+        self._pages[scene] = []
+        self._len = lens
+        self._news.release(scene)
         if stream is not None:
             self._hold(stream)
 
