@@ -417,3 +417,14 @@ def test_a_failed_send_leaves_the_books_as_they_were(lib, monkeypatch):
     assert [x for x in c.page_table.flatten().tolist() if x >= 0] == used
     c.release(0)
     assert sorted(c._free) == sorted(set(range(6)) - set(c._pages[1])) and c.lens.tolist() == [0, 32]
+
+
+def test_grow_refuses_parts_of_tokens(lib):
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(2, 1, tokens=64, page=16, device="cpu")
+    for n in ([1.5, 0], np.array([0.0, 0.5])):
+        with pytest.raises(ValueError):
+            c.grow(n)
+    assert c.lens.tolist() == [0, 0]
+    c.grow([2.0, np.float32(3)])
+    assert c.lens.tolist() == [2, 3] and c._len == [2, 3]

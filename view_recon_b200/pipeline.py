@@ -490,8 +490,8 @@ class FrameCache:
         before the layers' appends.  Lengths and table change on `stream` (default: the device's current one),
         in order with the calls there.  Raises MemoryError, changing nothing, when pages run out."""
         there = self._owned(stream)
-        ns = [n] * self.scenes if isinstance(n, numbers.Integral) else [int(x) for x in n]
-        if len(ns) != self.scenes or min(ns) < 0:
+        ns = [n] * self.scenes if isinstance(n, numbers.Integral) else list(n)
+        if len(ns) != self.scenes or any(int(x) != x for x in ns) or min(ns) < 0:
             raise ValueError("grow needs one non-negative count, or one per scene")
         lens = [have + int(x) for have, x in zip(self._len, ns)]
         if max(lens) > self.max_pages * self.page:
