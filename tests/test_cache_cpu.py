@@ -428,3 +428,12 @@ def test_grow_refuses_parts_of_tokens(lib):
     assert c.lens.tolist() == [0, 0]
     c.grow([2.0, np.float32(3)])
     assert c.lens.tolist() == [2, 3] and c._len == [2, 3]
+
+
+def test_a_cache_like_another_is_on_its_device(lib):
+    from view_recon_b200.pipeline import FrameCache
+    c = FrameCache(1, 1, tokens=64, page=16, device="cpu")
+    for device in ("cuda", "cuda:1", "meta"):
+        with pytest.raises(ValueError, match="device"):
+            FrameCache(1, 1, tokens=64, page=16, like=c, device=device)
+    assert FrameCache(1, 1, tokens=64, page=16, like=c, device="cpu").device == c.device

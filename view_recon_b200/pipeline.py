@@ -411,6 +411,8 @@ class FrameCache:
         if like is not None:
             if (like.scenes, like.page, like.max_pages) != (scenes, page, max_pages) or n_pages not in (None, like.n_pages):
                 raise ValueError("a cache like another has its scenes, page size, length and pages")
+            if device is not None and torch.device(device) not in (like.device, torch.device(like.device.type)):
+                raise ValueError("a cache like another is on its device, %s" % like.device)
             n_pages, device = like.n_pages, like.device
         n_pages = scenes * max_pages if n_pages is None else int(n_pages)
         dev = torch.device(device if device is not None else "cuda")
