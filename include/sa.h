@@ -398,7 +398,9 @@ sa_status sa_kv_append(const sa_kv_cache* cache, sa_dtype dtype, const void* k, 
  * Read rows back: row r < m of scene s (m as for sa_kv_append) is token start[s] + r, or
  * lens[s] - m + r without `start` (DEVICE int32 [scenes]).  k, v: [scenes * heads][n][64] of
  * `dtype`, either of them NULL to leave it out.  Exact in both types.  Rows r >= m, rows whose
- * token is outside [0, lens[s]) and rows on a bad page are left as they were.
+ * token is outside [0, lens[s]) and rows on a bad page are left as they were.  Rows that are read and
+ * written again are the same numbers with 8 bits; with 4 bits a number may move by up to half a step
+ * each time (the rounded block may take a smaller scale), so move pages, not rows.
  */
 sa_status sa_kv_read(const sa_kv_cache* cache, sa_dtype dtype, int32_t n, const int32_t* n_len_or_null,
                      const int32_t* start_or_null, const int32_t* lens, const int32_t* page_table,

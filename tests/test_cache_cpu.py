@@ -437,3 +437,23 @@ def test_a_cache_like_another_is_on_its_device(lib):
         with pytest.raises(ValueError, match="device"):
             FrameCache(1, 1, tokens=64, page=16, like=c, device=device)
     assert FrameCache(1, 1, tokens=64, page=16, like=c, device="cpu").device == c.device
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_writing_what_was_read(bits):
+    """8 bits: the same numbers again.  4 bits: not always (once the largest code is 7 a smaller scale may do: 14/15
+    of s reaches 7 s), but each within half a step of what was read, and a block's largest stays its largest."""
+    rng = np.random.default_rng(40 + bits)
+    x = rng.standard_normal((400, 64)) * np.exp(2 * rng.standard_normal((400, 1)))
+    y = orc.cache_numbers(x, bits)
+    z = orc.cache_numbers(y, bits)
+    if bits == 8:
+        assert np.array_equal(z, y)
+        return
+    blocks = [a.reshape(400, 4, 16) for a in (y, z)]
+    most = np.abs(blocks[0]).max(-1, keepdims=True)
+    # the smallest scale with 7.5 s >= most is below most / 7.5 * 9/8
+    assert (np.abs(blocks[1] - blocks[0]) <= most / 7.5 * 9 / 16).all()
+    assert (z != y).any()
+    at = np.abs(blocks[0]).argmax(-1)[..., None]
+    assert (np.take_along_axis(np.abs(blocks[1]), at, -1) == np.abs(blocks[1]).max(-1, keepdims=True)).all()
