@@ -330,7 +330,7 @@ __device__ __forceinline__ void note_parts(const AttnArgs& a, const Cut& cut, Wa
 
 // ------------------------------------------------------------------------------ few rows
 //
-// Up to 32 query rows a problem (48 in two): every page is read and decoded for few products, so the
+// Up to 32 query rows a problem (33 to 48 in two of 24, each decoding every key): every page is read and decoded for few products, so the
 // rows ride on the narrow side of mma.sync (m16n8k16, keys on m, rows on n): S^T = K Q^T with 16 keys x
 // 8 rows, O^T += V^T P^T with 16 channels x 8 rows (tcgen05 would take 128 rows, mostly padding, and
 // operands through shared memory).  A lane's decoded words are its operand registers as they stand (the
@@ -338,13 +338,16 @@ __device__ __forceinline__ void note_parts(const AttnArgs& a, const Cut& cut, Wa
 // the tensor cores; P^T is transposed by one movmatrix per 8 x 8.
 // Four warps take 32 keys each of every 128-key tile; a fifth keeps a ring of tiles in flight with
 // bulk copies of whole pages (K, V and scales of a page and head are one run of bytes).
-// Measured, 16 heads: 5 rows over 351 744 tokens in 4 bits 103 us, 3.9 TB/s, bound by instruction issue
-// (65 % of the slots, the ALU pipe 57 %; 1483 warp instructions a tile; the same ring with nothing done
-// to the tiles takes 73 us, everything but the decoding 76 us).  In 8 bits, with more bytes to the
-// instruction, 5.8 TB/s; with 12 rows 5.0 TB/s.
-// Blocks an SM, by groups of 8 rows: 4, 3, 2, 2 (what the registers allow without spills).  One group
-// with 5 blocks and 3 stages: 111 us against 104; two groups with 4: 174 against 133; four groups
-// with 3: 324 against 241.
+// Measured in a recorded graph, 16 heads over 351 744 tokens: in 4 bits 5 rows 100 us, 4.05 TB/s, 12 rows 131,
+// 24 rows 178, 32 rows 226 us; in 8 bits 5 rows 124 us, 6.2 TB/s, 12 rows 147 us, 5.2 TB/s, 32 rows 244 us.
+// 4 bits are bound by the decoding's instructions (65 % of the issue slots, the ALU pipe 57 %; 1483 warp
+// instructions a tile; the same ring with nothing done to the tiles takes 73 us, everything but the decoding
+// 76 us) and, with 20 warps an SM, by what latency the other third of the slots waits for.
+// Blocks an SM, by groups of 8 rows: 4, 3, 2, 2.  One group with 5 blocks and 3 stages: 111 us against 104;
+// two groups with 4: 174 against 133; four groups with 3: 324 against 241.  Registers a thread 96, 128, 168,
+// 168: one and two groups do not spill.  Two blocks of five warps put three warps on one quarter of an SM,
+// which leaves each 168, and there three groups spill 20 bytes (8 in 8 bits) and four groups 228 (loaded again:
+// 364, 360).  What one block an SM, with registers enough, would take has not been measured.
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {

@@ -17,6 +17,12 @@
 // and key).  No one unit is full: exponentials 59 % of the XU pipe, tensor pipe 30 %, issue 51 %, DRAM 5 %; each
 // half's chain (scores, maximum, exponentials, P, product) waits on its own hand-offs, and the other half
 // fills only part of them.  Without any exponential 250 us of 382 (1 280 rows over 43 968 tokens).
+// The sparse layer's kernel does 396 kFLOP a cycle where this one does 349: part of the difference is the last
+// row tile of a frame, 94 rows of 1 374 that cost 6/8 of a tile of 256.
+// Problems of at most 128 rows: 49, 64, 96 and 128 rows over 175 872 tokens all take 220 us in 4 bits and 264 us
+// in 8 bits (48 rows in the few-rows kernel: 177 and 189 us).  The time is the decoding's, not the rows': one
+// warpgroup reads pages from global memory a tile ahead, and padded rows take part in softmax and products.
+// The split leaves 100 bytes of spills a thread (272 loaded again).
 // Other shapes of the same work were slower: 2 blocks an SM of 128 rows with a decode of their own 1039 us,
 // three slots with 64-key steps 1131, two threads a row 976, the halves taking turns at the exponentials
 // 1004, exponentials of 1 to 4 of 8 pairs on the FMA pipe +8 to +15 %.

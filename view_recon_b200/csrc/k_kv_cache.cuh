@@ -298,8 +298,10 @@ __device__ __forceinline__ uint32_t pack_word(const float2* n) {
 // One thread: 16 channels of a token pair, K and V: the maximum of a scale's 16 channels is a thread's
 // own, and no thread shares a word with another.  Bound by its arithmetic at first (17 instructions an
 // element, 3.0 TB/s of bf16 into 4 bits); packed f32 pairs, three-input maxima and packing by
-// multiply-add leave about 8.  65 536 tokens x 16 heads, reading and writing together: bf16 into 4 bits
-// 65 us, 5.3 TB/s (issue 75 %, DRAM 62 % of its peak), into 8 bits 73 us; f32 into 4 bits 113 us, 8 bits 102.
+// multiply-add leave about 8.  65 536 tokens x 16 heads in a recorded graph (bytes read and written):
+// bf16 into 4 bits 61 us, 5.6 TB/s (issue 75 %, DRAM 62 % of its peak), into 8 bits 70 us, 5.9 TB/s; f32 into
+// 4 bits 109 us, 5.6 TB/s, 8 bits 99 us, 6.9 TB/s.  Four blocks an SM for bf16 into 4
+// bits (three for the others) make it spill 48 bytes a thread, three make f32 into 4 bits spill 152; 8 bits have none.
 template <int BITS, typename T>
 __global__ void __launch_bounds__(256, BITS == 4 && sizeof(T) == 2 ? 4 : 3) append_kernel(const CacheArgs a) {
     using F = Fmt<BITS>;
@@ -409,7 +411,8 @@ __device__ __forceinline__ void store16(T* dst, int wide, const uint32_t (&w)[8]
 }
 
 // One thread: 16 channels of a token pair, K and V (the writing kernel's mapping).  Bound by its writes:
-// 65 536 tokens x 16 heads from 4 bits to bf16 57 us, 6.0 TB/s, from 8 bits 67 us; to f32 96 and 106 us.
+// 65 536 tokens x 16 heads in a recorded graph, from 4 bits to bf16 56 us, 6.1 TB/s, from 8 bits 66 us, 6.3 TB/s;
+// to f32 95 and 104 us, 6.4 and 6.5 TB/s.
 template <int BITS, typename T>
 __global__ void __launch_bounds__(256) read_kernel(const CacheArgs a) {
     using F = Fmt<BITS>;

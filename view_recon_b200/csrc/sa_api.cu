@@ -1365,9 +1365,12 @@ dim3 kv_rows_grid(const sa_kv_cache* c, int32_t n) {
 
 // Query rows of one problem: all rows of a key head's query heads together in the smallest tile of
 // the few-rows kernel that holds them, or two of 24, or 256 at a time in the tcgen05 kernel.  Both sides
-// of the border, 16 heads in 4 bits: 48 rows over 30 011 tokens 39.6 us in two tiles of 24 and 48.5 us
-// there, 64 rows 51.6 us in two tiles of 32 and 48.8 us there (over 175 872 tokens 174 against 209 us, and
-// 231 against 210 us).
+// of the border, 16 heads, caches larger than L2, us in a recorded graph (4 bits, 8 bits):
+//   48 rows in two tiles of 24   30 011 tokens 42, 45   175 872 tokens 177, 189
+//   48 rows there                              57, 65                  219, 264
+//   64 rows in two tiles of 32                 52, 57                  225, 242
+//   64 rows there                              58, 65                  220, 264
+// (so from 49 to 64 rows 8 bits, and short caches, would still be better off in two tiles of 32)
 int32_t kv_tile_rows(int64_t rows) {
     if (rows <= 32) return (int32_t)std::max<int64_t>(8, (rows + 7) / 8 * 8);
     if (rows <= 48) return 24;
