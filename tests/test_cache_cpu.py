@@ -410,6 +410,11 @@ def test_a_failed_send_leaves_the_books_as_they_were(lib, monkeypatch):
         with pytest.raises(RuntimeError, match="no memory"):
             c.grow([20, 0])
         assert books() == before
+    table, calls, failing = c.page_table.clone(), [], 1
+    monkeypatch.setattr(c, "_send", fail)
+    with pytest.raises(RuntimeError, match="no memory"):
+        c.release(0)
+    assert books() == before and c.page_table.equal(table)
     monkeypatch.setattr(c, "_send", send)
     c.grow([44, 29])                                       # all six pages, each once
     used = [p for pages in c._pages for p in pages]

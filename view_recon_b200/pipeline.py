@@ -527,8 +527,8 @@ class FrameCache:
         lens = list(self._len)
         lens[scene] = 0
         with there:
+            self._send_lengths(lens)   # (first: should it fail, the table is as it was)
             self.page_table[scene].fill_(-1)
-            self._send_lengths(lens)
         self._free.extend(reversed(self._pages[scene]))
         self._pages[scene] = []
         self._len = lens
