@@ -883,3 +883,31 @@ def test_binding_calls_and_layer_objects_agree(rows):
                             orc.cache_numbers(k[s * heads:(s + 1) * heads, :m], 4)], 1)
         mine = slice(s * heads, (s + 1) * heads)
         _same((layer.o[mine], layer.lse[mine]), orc.cache_attend(q[mine], K, K, 0.125))
+
+
+def test_recording_a_write_is_not_a_write():
+    """A graph recorded between two grows: the tokens of both are still to be written, together or by the replay."""
+    import torch
+    from view_recon_b200.pipeline import FrameCache
+    rng = np.random.default_rng(26)
+    c = FrameCache(1, 2, tokens=64, page=16)
+    k, tk = _rows(rng, (2, 9, 64), "bf16")
+    part = tk[:, :5].contiguous()
+    c.grow(5)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        c.append(tk, tk)                 # nine rows, of which five have been counted in by now
+    c.grow(4)
+    c.append(tk, tk)
+    out, _ = c.read(torch.empty_like(tk), torch.empty_like(tk))
+    _ok()
+    assert np.array_equal(H.from_device(out), orc.cache_numbers(k, 4))
+    with pytest.raises(ValueError):
+        c.append(part, part)
+    c.release(0)
+    c.grow(9)
+    g.replay()
+    out, _ = c.read(torch.empty_like(tk), torch.empty_like(tk))
+    _ok()
+    assert np.array_equal(H.from_device(out), orc.cache_numbers(k, 4))

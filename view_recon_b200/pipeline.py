@@ -581,11 +581,13 @@ class FrameCache:
         pv = _want("v", v, shape, (k.dtype,), self.device)
         if n == 0:
             return
-        if self._news is not None:
-            if new_len is None and n not in self._news.fits and not self._recording(stream):
+        news = self._news
+        if news is not None:
+            if new_len is not None or n in news.fits:
+                news.appended = True
+            elif not self._recording(stream):  # (a recorded call writes when it is replayed)
                 raise ValueError("%d rows for every scene, but the last grow counted in %s: rows of other counts "
-                                 "need new_len" % (n, self._news.last))
-            self._news.appended = True
+                                 "need new_len" % (n, news.last))
         self._call(sa.load().sa_kv_append, sa.SA_BF16 if k.dtype is self._types[0] else sa.SA_F32, pk, pv, n,
                    self._counts("new_len", new_len), self.lens.data_ptr(), self.page_table.data_ptr(),
                    self.pool.data_ptr(), stream=stream)
